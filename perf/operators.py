@@ -322,8 +322,8 @@ def _own_attn(s):
             s["out"], s["lse"], s["ws"], s["ws"].numel(), s["status"])
     else:
         abi.tidar_attn_step_shared(
-            s["q"], s["kn"], s["vn"], s["ks"], s["vs"], s["shared_len"], s["kc"], s["vc"], s["prefix_len"], B, Hq,
-            Hkv, D, k, R, S, P, scale, mode, s["out"], s["lse"], s["ws"], s["ws"].numel(), s["status"])
+            s["q"], s["kn"], s["vn"], s["ks"], s["vs"], s["shared_len"], S, s["kc"], s["vc"], s["prefix_len"], B, Hq,
+            Hkv, D, k, R, P, scale, mode, s["out"], s["lse"], s["ws"], s["ws"].numel(), s["status"])
     return s["out"], s["lse"]
 
 
