@@ -41,6 +41,12 @@ _SIGS = {
     "tidar_pick_draft_length": (_i, [_vp, _i, ctypes.c_double, _vp]),
     "tidar_attn_step_paged": (_i, [_vp] * 6 + [_i, _i, _vp] + [_i] * 5 + [_f, _i] + [_vp, _vp, _vp, _vp]),
     "tidar_kv_commit_paged": (_i, [_vp] * 5 + [_i] * 7 + [_vp] * 4 + [_i, _i, _vp] + [_vp] * 4 + [_sz, _vp, _vp]),
+    "tidar_attn_shared_workspace_size": (_sz, [_i] * 7),
+    "tidar_attn_step_shared": (_i, [_vp] * 6 + [_i] + [_vp] * 3 + [_i] * 7 + [_f, _i] + [_vp] * 3 + [_sz, _vp, _vp]),
+    "tidar_attn_step_shared_paged": (_i, [_vp] * 6 + [_i, _vp, _vp, _i, _i, _vp] + [_i] * 6 + [_f, _i] + [_vp] * 3
+                                     + [_sz, _vp, _vp]),
+    "tidar_attn_mass": (_i, [_vp] * 5 + [_i, _i, _vp, _vp] + [_i] * 7 + [_f, _f, _vp, _vp]),
+    "tidar_kv_evict": (_i, [_vp] * 4 + [_i, _i, _vp] + [_i] * 8 + [_vp, _vp]),
     "tidar_rope_qkv": (_i, [_vp, _vp] + [_i] * 5 + [ctypes.c_double] + [_vp] * 5),
     "tidar_verify_commit_workspace_size": (_sz, [_i] * 3),
     "tidar_verify_commit": (_i, [_vp, _vp, _i] + [_vp] * 4 + [_f] + [_vp] * 5 + [_i] * 9 + [_vp] * 12
@@ -113,6 +119,47 @@ def tidar_kv_commit_paged(k_pools, v_pools, k_news, v_news, block_table, max_pag
         D, k, _ptr(prefix_len), _ptr(accept_len), _ptr(resampled), _ptr(group_logits), logits_dtype, V,
         _ptr(u_draft), _ptr(next_drafts), _ptr(next_preaccepted), _ptr(next_q_group), _ptr(workspace), ws_bytes,
         _ptr(dev_status), _stream(stream)))
+
+
+def tidar_attn_shared_workspace_size(B, Hq, Hkv, D, R, S_max, P_max) -> int:
+    return _lib.tidar_attn_shared_workspace_size(B, Hq, Hkv, D, R, S_max, P_max)
+
+
+def tidar_attn_step_shared(q, k_new, v_new, k_shared, v_shared, shared_len, S_max, k_cache, v_cache, prefix_len, B,
+                           Hq, Hkv, D, k, R, P_max, softmax_scale, mask_mode, out, lse, workspace, ws_bytes,
+                           dev_status, stream=None) -> None:
+    """Attention of a batch behind one shared prefix, which is stored and multiplied once."""
+    _check("tidar_attn_step_shared", _lib.tidar_attn_step_shared(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_shared), _ptr(v_shared), _ptr(shared_len), S_max, _ptr(k_cache),
+        _ptr(v_cache), _ptr(prefix_len), B, Hq, Hkv, D, k, R, P_max, softmax_scale, mask_mode, _ptr(out), _ptr(lse),
+        _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream)))
+
+
+def tidar_attn_step_shared_paged(q, k_new, v_new, k_pool, v_pool, shared_table, max_shared_pages, shared_len,
+                                 block_table, max_pages, num_pages, prefix_len, B, Hq, Hkv, D, k, R, softmax_scale,
+                                 mask_mode, out, lse, workspace, ws_bytes, dev_status, stream=None) -> None:
+    _check("tidar_attn_step_shared_paged", _lib.tidar_attn_step_shared_paged(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(shared_table), max_shared_pages,
+        _ptr(shared_len), _ptr(block_table), max_pages, num_pages, _ptr(prefix_len), B, Hq, Hkv, D, k, R,
+        softmax_scale, mask_mode, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status),
+        _stream(stream)))
+
+
+def tidar_attn_mass(qs, lses, k_caches, masses, block_table, max_pages, num_pages, prefix_len, row_count, L, B, Hq,
+                    Hkv, D, R, P_max, softmax_scale, decay, dev_status, stream=None) -> None:
+    """The attention weight the newest tokens gave to every cache row, added to its running sum (all layers)."""
+    _check("tidar_attn_mass", _lib.tidar_attn_mass(
+        _ptr(qs), _ptr(lses), _ptr(k_caches), _ptr(masses), _ptr(block_table), max_pages, num_pages,
+        _ptr(prefix_len), _ptr(row_count), L, B, Hq, Hkv, D, R, P_max, softmax_scale, decay, _ptr(dev_status),
+        _stream(stream)))
+
+
+def tidar_kv_evict(k_caches, v_caches, masses, block_table, max_pages, num_pages, prefix_len, L, B, Hkv, D, P_max,
+                   budget, sink, recent, dev_status, stream=None) -> None:
+    """Caches longer than `budget` rows give up their rows of least mass, in place (all layers)."""
+    _check("tidar_kv_evict", _lib.tidar_kv_evict(
+        _ptr(k_caches), _ptr(v_caches), _ptr(masses), _ptr(block_table), max_pages, num_pages, _ptr(prefix_len), L, B,
+        Hkv, D, P_max, budget, sink, recent, _ptr(dev_status), _stream(stream)))
 
 
 def tidar_rope_qkv(qkv, prefix_len, B, Hq, Hkv, D, k, theta, q, k_new, v_new, dev_status, stream=None) -> None:
@@ -213,7 +260,8 @@ def tidar_pick_draft_length(step_us, alpha):
 
 
 def pointer_array(tensors, device):
-    """Device int64 array holding the data pointers of `tensors` (for tidar_kv_commit)."""
+    """Device int64 array holding the data pointers of `tensors` (for tidar_kv_commit, tidar_attn_mass and
+    tidar_kv_evict)."""
     import torch
     return torch.tensor([t.data_ptr() for t in tensors], dtype=torch.int64, device=device)
 

@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "attn.cuh"
+#include "cache_ops.cuh"
 #include "../../include/tidar_testing.h"
 
 namespace tidar {
@@ -284,6 +285,172 @@ tidar_status tidar_verify_commit(const void *p_logits, const void *q_logits, int
                                          P_max, V, prefix_len, group_logits, u_draft, accept_len, resampled, tokens,
                                          n_emitted, logp_d, logq_d, next_drafts, next_preaccepted, next_q_group,
                                          workspace, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Sizes of the shared-prefix attention that do not depend on the layout of the caches.
+tidar_status check_shared(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || R < 1 || S_max < 0 || P_max < 0) return TIDAR_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128) || B > kMaxBatchShared || R > kMaxCausalRows)
+        return TIDAR_ERR_UNSUPPORTED;
+    if ((long long)B * R * Hq >= (1LL << 31)) return TIDAR_ERR_UNSUPPORTED;
+    return TIDAR_OK;
+}
+
+tidar_status attn_shared(SharedAttnParams p, int S_max, int P_max, size_t ws_bytes, float softmax_scale, void *stream) {
+    if (!p.q || !p.k_new || !p.v_new || !p.shared_len || !p.prefix_len || !p.out || !p.dev_status)
+        return TIDAR_ERR_INVALID_ARG;
+    if (!aligned16(p.q) || !aligned16(p.k_new) || !aligned16(p.v_new) || !aligned16(p.k_shared) ||
+        !aligned16(p.v_shared) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.out) ||
+        (p.lse && (reinterpret_cast<uintptr_t>(p.lse) & 3)))
+        return TIDAR_ERR_INVALID_ARG;
+    if (p.mask_mode == TIDAR_MASK_HYBRID) {
+        if (p.k < 1) return TIDAR_ERR_INVALID_ARG;
+        if (p.k > kMaxDraft) return TIDAR_ERR_UNSUPPORTED;
+        if (p.R != p.k * (p.k + 2)) return TIDAR_ERR_INVALID_ARG;
+    } else if (p.mask_mode != TIDAR_MASK_CAUSAL) {
+        return TIDAR_ERR_INVALID_ARG;
+    }
+    if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return TIDAR_ERR_INVALID_ARG;
+    const size_t need = shared_attn_workspace_bytes(p.B, p.Hq, p.Hkv, p.D, p.R, S_max, P_max);
+    if (need > 0) {
+        if (!p.ws || !aligned256(p.ws)) return TIDAR_ERR_INVALID_ARG;
+        if (ws_bytes < need) return TIDAR_ERR_WORKSPACE;
+    }
+    p.G = p.Hq / p.Hkv;
+    p.S_max = S_max;
+    p.P_max = P_max;
+    p.scale_log2 = softmax_scale * kLog2e;
+    return launched(shared_attn_launch(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max) {
+    if (check_shared(B, Hq, Hkv, D, R, S_max, P_max) != TIDAR_OK) return 0;
+    return shared_attn_workspace_bytes(B, Hq, Hkv, D, R, S_max, P_max);
+}
+
+tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void *v_new, const void *k_shared,
+                                    const void *v_shared, const int32_t *shared_len, int S_max, const void *k_cache,
+                                    const void *v_cache, const int32_t *prefix_len, int B, int Hq, int Hkv, int D,
+                                    int k, int R, int P_max, float softmax_scale, int mask_mode, void *out, float *lse,
+                                    void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream) {
+    const tidar_status st = check_shared(B, Hq, Hkv, D, R, S_max, P_max);
+    if (st != TIDAR_OK) return st;
+    if ((long long)Hkv * S_max >= (1LL << 31) || (long long)B * Hkv * P_max >= (1LL << 31))
+        return TIDAR_ERR_UNSUPPORTED;
+    if (S_max > 0 && (!k_shared || !v_shared)) return TIDAR_ERR_INVALID_ARG;
+    if (P_max > 0 && (!k_cache || !v_cache)) return TIDAR_ERR_INVALID_ARG;
+    SharedAttnParams p{};
+    p.q = static_cast<const bf16 *>(q);
+    p.k_new = static_cast<const bf16 *>(k_new);
+    p.v_new = static_cast<const bf16 *>(v_new);
+    p.k_shared = static_cast<const bf16 *>(k_shared);
+    p.v_shared = static_cast<const bf16 *>(v_shared);
+    p.k_cache = static_cast<const bf16 *>(k_cache);
+    p.v_cache = static_cast<const bf16 *>(v_cache);
+    p.shared_len = shared_len;
+    p.prefix_len = prefix_len;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.k = k;
+    p.R = R;
+    p.mask_mode = mask_mode;
+    p.out = static_cast<bf16 *>(out);
+    p.lse = lse;
+    p.ws = static_cast<uint8_t *>(workspace);
+    p.dev_status = dev_status;
+    return attn_shared(p, S_max, P_max, ws_bytes, softmax_scale, stream);
+}
+
+tidar_status tidar_attn_step_shared_paged(const void *q, const void *k_new, const void *v_new, const void *k_pool,
+                                          const void *v_pool, const int32_t *shared_table, int max_shared_pages,
+                                          const int32_t *shared_len, const int32_t *block_table, int max_pages,
+                                          int num_pages, const int32_t *prefix_len, int B, int Hq, int Hkv, int D,
+                                          int k, int R, float softmax_scale, int mask_mode, void *out, float *lse,
+                                          void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream) {
+    if (!block_table || max_pages < 1 || num_pages < 1 || max_shared_pages < 0) return TIDAR_ERR_INVALID_ARG;
+    if (max_shared_pages > 0 && !shared_table) return TIDAR_ERR_INVALID_ARG;
+    if (max_pages > kMaxPagesPerSeq || max_shared_pages > kMaxSharedPages) return TIDAR_ERR_UNSUPPORTED;
+    const int S_max = max_shared_pages * kPageRows, P_max = max_pages * kPageRows;
+    const tidar_status st = check_shared(B, Hq, Hkv, D, R, S_max, P_max);
+    if (st != TIDAR_OK) return st;
+    if ((long long)num_pages * Hkv * kPageRows >= (1LL << 31)) return TIDAR_ERR_UNSUPPORTED;
+    if (!k_pool || !v_pool) return TIDAR_ERR_INVALID_ARG;
+    SharedAttnParams p{};
+    p.q = static_cast<const bf16 *>(q);
+    p.k_new = static_cast<const bf16 *>(k_new);
+    p.v_new = static_cast<const bf16 *>(v_new);
+    p.k_shared = p.k_cache = static_cast<const bf16 *>(k_pool);
+    p.v_shared = p.v_cache = static_cast<const bf16 *>(v_pool);
+    p.shared_len = shared_len;
+    p.prefix_len = prefix_len;
+    p.shared_table = shared_table;
+    p.block_table = block_table;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.k = k;
+    p.R = R;
+    p.mask_mode = mask_mode;
+    p.out = static_cast<bf16 *>(out);
+    p.lse = lse;
+    p.ws = static_cast<uint8_t *>(workspace);
+    p.dev_status = dev_status;
+    return attn_shared(p, S_max, P_max, ws_bytes, softmax_scale, stream);
+}
+
+tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, const void *const *k_caches,
+                             float *const *masses, const int32_t *block_table, int max_pages, int num_pages,
+                             const int32_t *prefix_len, const int32_t *row_count, int L, int B, int Hq, int Hkv,
+                             int D, int R, int P_max, float softmax_scale, float decay, int32_t *dev_status,
+                             void *stream) {
+    if (L < 1 || B < 1 || Hq < 1 || Hkv < 1 || R < 1) return TIDAR_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || (D != 64 && D != 128) || B > kMaxBatchShared) return TIDAR_ERR_UNSUPPORTED;
+    if (block_table) {
+        if (max_pages < 1 || num_pages < 1) return TIDAR_ERR_INVALID_ARG;
+        if (max_pages > kMaxPagesPerSeq) return TIDAR_ERR_UNSUPPORTED;
+        P_max = max_pages * kPageRows;
+    } else if (P_max < 0) {
+        return TIDAR_ERR_INVALID_ARG;
+    }
+    if (P_max > kMaxMassRows || (long long)R * Hq >= (1LL << 31) || (long long)L * Hkv >= (1LL << 16) / 2)
+        return TIDAR_ERR_UNSUPPORTED;
+    if (!qs || !lses || !k_caches || !masses || !prefix_len || !dev_status) return TIDAR_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return TIDAR_ERR_INVALID_ARG;
+    if (!std::isfinite(decay) || !(decay >= 0.f)) return TIDAR_ERR_INVALID_ARG;
+    MassParams p{qs, lses, k_caches, masses, block_table, block_table ? max_pages : 0, block_table ? num_pages : 0,
+                 prefix_len, row_count, L, B, Hq, Hkv, D, R, Hq / Hkv, P_max, softmax_scale * kLog2e, decay,
+                 dev_status};
+    return launched(mass_launch(p, static_cast<cudaStream_t>(stream)));
+}
+
+tidar_status tidar_kv_evict(void *const *k_caches, void *const *v_caches, float *const *masses,
+                            const int32_t *block_table, int max_pages, int num_pages, int32_t *prefix_len, int L,
+                            int B, int Hkv, int D, int P_max, int budget, int sink, int recent, int32_t *dev_status,
+                            void *stream) {
+    if (L < 1 || B < 1 || Hkv < 1) return TIDAR_ERR_INVALID_ARG;
+    if (budget < 0 || sink < 0 || recent < 0 || (long long)sink + recent > budget) return TIDAR_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return TIDAR_ERR_UNSUPPORTED;
+    if (block_table) {
+        if (max_pages < 1 || num_pages < 1) return TIDAR_ERR_INVALID_ARG;
+        if (max_pages > kMaxPagesPerSeq) return TIDAR_ERR_UNSUPPORTED;
+        P_max = max_pages * kPageRows;
+    } else if (P_max < 0) {
+        return TIDAR_ERR_INVALID_ARG;
+    }
+    if (P_max > kMaxEvictRows || (long long)L * B * Hkv > (1LL << 27)) return TIDAR_ERR_UNSUPPORTED;
+    if (!k_caches || !v_caches || !masses || !prefix_len || !dev_status) return TIDAR_ERR_INVALID_ARG;
+    EvictParams p{k_caches, v_caches, masses, block_table, block_table ? max_pages : 0, block_table ? num_pages : 0,
+                  prefix_len, L, B, Hkv, D, P_max, budget, sink, recent, dev_status};
+    return launched(evict_launch(p, static_cast<cudaStream_t>(stream)));
 }
 
 const char *tidar_status_string(tidar_status s) {

@@ -13,7 +13,9 @@
  *   tidar_attn_step   the structured hybrid-mask attention of one layer;
  *   tidar_verify      the AR rejection-sampling verify of the drafts;
  *   tidar_kv_commit   the exact-KV-cache commit/evict + next-draft selection;
- * tidar_verify_commit makes the last two in one launch.
+ * tidar_verify_commit makes the last two in one launch.  A batch that shares a
+ * long prefix takes tidar_attn_step_shared; tidar_attn_mass and tidar_kv_evict
+ * keep the caches within a fixed number of rows.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -139,6 +141,76 @@ tidar_status tidar_attn_step_paged(const void *q, const void *k_new, const void 
                                    int max_pages, int num_pages, const int32_t *prefix_len,
                                    int B, int Hq, int Hkv, int D, int k, float softmax_scale,
                                    int mask_mode, void *out, float *lse, int32_t *dev_status, void *stream);
+
+/* Bytes of device scratch tidar_attn_step_shared (and its paged form, with
+ * S_max = 64 * max_shared_pages and P_max = 64 * max_pages) needs for these
+ * sizes; 0 for sizes those calls reject. */
+size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max);
+
+/*
+ * One layer of attention for a batch whose sequences all start with the same
+ * S tokens (a system prompt, few-shot examples, a document asked about B
+ * times), stored once.
+ *
+ * Defined by: as tidar_attn_step; the batch is the serving case the TiDAR
+ * summary leaves to future work ("局限与 Future Work": batch > 1, prefix
+ * caching).  The keys of sequence b, in order:
+ *   [shared rows 0..S-1 | cache rows 0..P_b-1 | the R new keys],
+ * with tidar_attn_step's masks on the new keys (every shared and every cached
+ * key is visible to every row).  The shared rows are read and multiplied once
+ * for the rows of all sequences together, however few rows one sequence has;
+ * the partial results of a row's shared keys and of its own keys are joined by
+ * their log-sum-exps.
+ *
+ * k_shared, v_shared  bf16 [Hkv, S_max, D]  rows 0..S-1 are used; whole 128-row
+ *             tiles are read, inside the buffer, and rows past S are ignored,
+ *             whatever they hold (NaN included); may be NULL when S_max is 0
+ * shared_len  int32 [1] (device)  S, 0 <= S <= S_max
+ * k_cache, v_cache, prefix_len  as in tidar_attn_step (own rows only: P_b does
+ *             not count the shared rows); the caches may be NULL when P_max is 0
+ * k, R        rows per sequence: TIDAR_MASK_HYBRID wants R = k(k+2), k in
+ *             1..16; TIDAR_MASK_CAUSAL takes any R in 1..4096 and ignores k
+ *             (R = 1 is plain decoding, one token per sequence; R > 1 also
+ *             scores or prefills R tokens)
+ * q, k_new, v_new, out, lse  as in tidar_attn_step, with R rows per sequence.
+ *             V rows multiply even a zero weight: a non-finite v_new, or a
+ *             non-finite visible cache row, reaches every row of its sequence
+ *             (a shared one, every row of the batch); masked k_new may hold
+ *             anything.
+ * workspace   >= tidar_attn_shared_workspace_size(...) bytes, 256-byte aligned
+ * dev_status  TIDAR_DEV_BAD_PREFIX: a prefix length out of range (that
+ *             sequence's rows are not written) or a shared length out of range
+ *             (no row is written).
+ * Hq/Hkv <= 128, B <= 1024, D in {64, 128}; Hkv * S_max, B * Hkv * P_max and
+ * B * R * Hq below 2^31 (else TIDAR_ERR_UNSUPPORTED).
+ */
+tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void *v_new,
+                                    const void *k_shared, const void *v_shared, const int32_t *shared_len,
+                                    int S_max, const void *k_cache, const void *v_cache,
+                                    const int32_t *prefix_len, int B, int Hq, int Hkv, int D, int k, int R,
+                                    int P_max, float softmax_scale, int mask_mode, void *out, float *lse,
+                                    void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * tidar_attn_step_shared over a paged KV cache (layout as in
+ * tidar_attn_step_paged): the shared rows live in pages of the same pools.
+ * Shared row n is row n % 64 of page shared_table[n / 64].
+ *
+ * shared_table  int32 [max_shared_pages] (device); 0 <= max_shared_pages <=
+ *               4096, S <= 64 * max_shared_pages; may be NULL when
+ *               max_shared_pages is 0
+ * block_table   int32 [B, max_pages], pages of each sequence's own rows
+ * A page id outside [0, num_pages) sets TIDAR_DEV_BAD_PAGE: among a sequence's
+ * own pages that sequence's rows are not written, among the shared pages none
+ * are.  Everything else as above.
+ */
+tidar_status tidar_attn_step_shared_paged(const void *q, const void *k_new, const void *v_new,
+                                          const void *k_pool, const void *v_pool, const int32_t *shared_table,
+                                          int max_shared_pages, const int32_t *shared_len,
+                                          const int32_t *block_table, int max_pages, int num_pages,
+                                          const int32_t *prefix_len, int B, int Hq, int Hkv, int D, int k, int R,
+                                          float softmax_scale, int mask_mode, void *out, float *lse,
+                                          void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
 
 /*
  * Rotary position embedding of one step's rows, fused with the re-layout of the
@@ -395,6 +467,92 @@ tidar_status tidar_verify_commit(const void *p_logits, const void *q_logits, int
                                  float *logp_d, float *logq_d, int32_t *next_drafts, uint8_t *next_preaccepted,
                                  int32_t *next_q_group, void *workspace, size_t ws_bytes, int32_t *dev_status,
                                  void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Bounded caches: attention mass and eviction                               */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Adds the attention weight that a step's accepted tokens gave to every cache
+ * row to a running sum per row, for all layers in one launch.
+ *
+ * Defined by: the softmax of tidar_attn_step; the pages name a bounded memory
+ * only as future work (summary, "局限与 Future Work": long contexts), so the
+ * statistic is the plain one, the column sums of the attention weights.
+ * Called after the commit: the a_b = row_count[b] newest tokens of sequence b
+ * are then its cache's last rows N-a_b..N-1 (N = prefix_len[b]), and their
+ * queries are rows 0..a_b-1 of q (the accepted drafts).  With
+ *   w(n) = sum over j < a_b with n <= N - a_b + j, and over the G = Hq/Hkv query
+ *          heads of KV head h, of exp(scale * q_j k_n - lse_j)
+ * the mass of cache row n (per layer, sequence and KV head) becomes
+ *   decay * mass + w(n)  for the rows that were there before, n < N - a_b, and
+ *   w(n)                 for the newest rows (whatever mass held there).
+ * mass rows N.. are not touched.  lse is the attention's own output, so keys
+ * outside the cache (a shared prefix, the rejected drafts) keep their share of
+ * each softmax; the weights of the cache rows then sum to less than 1 per row.
+ * Every row's sum is taken by one thread in a fixed order: results do not
+ * depend on timing.
+ *
+ * qs        device array of L device pointers, bf16 [B, R, Hq, D] each
+ * lses      device array of L device pointers, f32 [B, R, Hq] each: the
+ *           natural-log LSE that tidar_attn_step* returned for those rows
+ * k_caches  device array of L device pointers: caches bf16 [B, Hkv, P_max, D],
+ *           or, with a block_table, pools [num_pages, Hkv, 64, D]
+ * masses    device array of L device pointers, f32 [B, Hkv, P_max] each (P_max =
+ *           64 * max_pages with a block_table), updated in place
+ * block_table  int32 [B, max_pages] or NULL (contiguous caches; max_pages and
+ *           num_pages are then ignored); P_max is ignored with a block_table
+ * prefix_len   int32 [B], after the commit
+ * row_count    int32 [B], 0..min(R, prefix_len[b]) (accept_len of the verify), or
+ *           NULL: R for every sequence
+ * R >= 1 rows per sequence in q and lse; decay finite and >= 0 (1: a plain sum).
+ * dev_status   TIDAR_DEV_BAD_PREFIX, TIDAR_DEV_BAD_ACCEPT (row_count) or
+ *           TIDAR_DEV_BAD_PAGE: that sequence's masses are left as they were.
+ * D in {64, 128}; B <= 1024, P_max <= 2^22, R * Hq < 2^31 and L * Hkv < 2^15 (else TIDAR_ERR_UNSUPPORTED);
+ * q and the caches 16-byte aligned (the pointers are on the device: not checked).
+ */
+tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, const void *const *k_caches,
+                             float *const *masses, const int32_t *block_table, int max_pages, int num_pages,
+                             const int32_t *prefix_len, const int32_t *row_count, int L, int B, int Hq, int Hkv,
+                             int D, int R, int P_max, float softmax_scale, float decay, int32_t *dev_status,
+                             void *stream);
+
+/*
+ * Brings every cache that is longer than `budget` rows down to `budget` rows,
+ * in place, giving up the rows with the least attention mass.
+ *
+ * Defined by: the exact-KV-cache bookkeeping of the commit (rows that leave the
+ * cache leave at once, summary §3.2); which rows leave is the choice that the
+ * accumulated attention weight of tidar_attn_mass makes.  For every layer,
+ * sequence and KV head with N = prefix_len[b] > budget:
+ *   - rows 0..sink-1 and the newest rows N-recent..N-1 always stay;
+ *   - of the rows between, the Z - sink with the greatest mass stay (Z = budget -
+ *     recent; among equals the lower row stays; NaN counts as greatest, -0 as 0);
+ *   - the surviving rows at Z..N-recent-1, in order, move into the places of the
+ *     evicted rows below Z, in order; then rows N-recent..N-1 move, in order, to
+ *     Z..budget-1.
+ * So rows that stay below Z do not move, only as many rows move as holes are to
+ * fill (plus the newest ones), and the cache's last `recent` rows are always the
+ * newest tokens in order, as the next call needs them.  Attention over cached
+ * rows does not depend on their order; the keys carry their own positions (RoPE
+ * is applied before the cache), and from the first eviction on the caller keeps
+ * the tokens' count for RoPE apart from prefix_len.  masses move with their rows.
+ * Rows budget.. keep what they held.  prefix_len[b] becomes budget.
+ *
+ * k_caches, v_caches  device arrays of L device pointers (bf16 caches or pools)
+ * masses              device array of L device pointers, f32 [B, Hkv, P_max]
+ * block_table, max_pages, num_pages, P_max  as for tidar_attn_mass
+ * prefix_len          int32 [B], read and updated in place
+ * budget, sink, recent >= 0 with sink + recent <= budget
+ * dev_status  TIDAR_DEV_BAD_PREFIX, TIDAR_DEV_BAD_PAGE: that sequence is left
+ *             untouched in every layer.
+ * D in {64, 128}; P_max <= 65536 (else TIDAR_ERR_UNSUPPORTED); the caches
+ * 16-byte aligned (the pointers are on the device: not checked).
+ */
+tidar_status tidar_kv_evict(void *const *k_caches, void *const *v_caches, float *const *masses,
+                            const int32_t *block_table, int max_pages, int num_pages, int32_t *prefix_len, int L,
+                            int B, int Hkv, int D, int P_max, int budget, int sink, int recent,
+                            int32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *tidar_status_string(tidar_status s);
