@@ -1,81 +1,772 @@
-// Attention of a batch behind one shared prefix: one warp per query row, online softmax over all its keys.
+// Attention of a batch behind one shared prefix (sm_100a: TMA + tcgen05, TMEM accumulators).
+//
+// out = softmax(scale q [K_shared | K_own | K_new]^T) [V_shared | V_own | V_new] is a sum over disjoint key sets, so it
+// is computed per set and joined by the sets' log-sum-exps: with (O_s, lse_s) a normalised partial row,
+// O = sum_s w_s O_s, w_s = exp(lse_s - lse), lse = log sum_s exp(lse_s).
+//
+// Work: a row tile is RT = floor(128 / G) rows (b, r) times the G query heads of one KV head.  Against the shared keys
+// the rows of all sequences are packed into row tiles together (that is what sharing buys: B R G rows multiply each
+// shared K/V byte); against its own cache and the new keys each sequence has row tiles of its own.  A block is two row
+// tiles (the last may be one) with all their key tiles of 128.  The blocks' key tiles form one line (per KV head: the
+// shared blocks, then each sequence's own), which is cut into equal shares of cost, one per CTA: every SM gets the same
+// work whatever the lengths, and a CTA's share is a few segments (block, run of key tiles).  Each segment leaves one
+// partial record; combine_kernel joins a row's records in a fixed order.  The line and its cuts follow from the lengths
+// alone, which every CTA reads on the device, so nothing waits on the host and nothing on timing.
+//
+// A CTA (12 warps): warp 0 streams K and V tiles by TMA through one ring; warp 2 loads Q; warp 1 issues every MMA;
+// warps 4-7 and 8-11 are the softmax of row tile 0 and 1 (thread = row = TMEM lane).  The two row tiles share each K/V
+// tile and run half a period apart: while one's softmax works, the tensor cores multiply for the other.
+// TMEM: S0 [0, 128), S1 [128, 256), O0 [256, 256 + D), O1 [256 + D, 256 + 2D).  P (bf16) overwrites the first 64 columns
+// of its S, so S = Q K of the next key tile is issued once the PV that reads P has completed.
 #include "cache_ops.cuh"
+#include "tc.cuh"
 
 namespace tidar {
 
 namespace {
 
-__global__ void __launch_bounds__(256) shared_attn_rows_kernel(const SharedAttnParams p) {
-    const int lane = threadIdx.x & 31;
-    const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const long rows = (long)p.B * p.R * p.Hq;
-    if (row >= rows) return;
-    const int h = (int)(row % p.Hq), r = (int)(row / p.Hq % p.R), b = (int)(row / p.Hq / p.R);
-    const int kvh = h / p.G, per = p.D / 32;
+constexpr int TM = 128;
+constexpr int TN = 128;
+constexpr int THREADS = 384;
+constexpr int BOXR = kPageRows;
+// Cost of one key tile for a block of two row tiles and of one.
+constexpr int kCostPair = 3, kCostSingle = 2;
+constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
+
+// What the line of key tiles is made of; CTA 0 leaves it in the workspace for combine_kernel, followed by cum[0..B]:
+// cum[b] = key tiles of the sequences before b.
+struct Line {
+    long long total;   // cost of all KV heads
+    long long head;    // cost of one KV head
+    long long shared;  // of its shared blocks
+    int shared_tiles;  // key tiles of the shared prefix
+    int pad;
+};
+constexpr int kLineBytes = 256;
+
+__host__ __device__ __forceinline__ int rows_per_tile(int G) { return TM / G; }
+__host__ __device__ __forceinline__ size_t info_bytes(int B) { return align256(kLineBytes + (size_t)(B + 1) * 4); }
+// One record: two row tiles, each [D/8 chunks][128 rows] 16-byte chunks of 8 fp16 and a header [128 rows] (log2 of the
+// row's sum, scale of its values).
+__host__ __device__ __forceinline__ size_t tile_record_bytes(int D) { return (size_t)TM * (D * 2 + 8); }
+
+struct Geometry {
+    int RT, shared_rt, shared_blocks, own_rt, own_blocks, blocks;  // (rt: row tiles; per KV head)
+};
+__host__ __device__ __forceinline__ Geometry geometry(int B, int R, int G) {
+    Geometry g;
+    g.RT = rows_per_tile(G);
+    g.shared_rt = ceil_div(B * R, g.RT);
+    g.shared_blocks = ceil_div(g.shared_rt, 2);
+    g.own_rt = ceil_div(R, g.RT);
+    g.own_blocks = ceil_div(g.own_rt, 2);
+    g.blocks = g.shared_blocks + B * g.own_blocks;
+    return g;
+}
+
+// First position of CTA c of n on a line of length total: the position s belongs to CTA floor(s n / total).
+__device__ __forceinline__ long long cut(long long total, int c, int n) { return (total * c + n - 1) / n; }
+
+// A block of the line: `tiles` key tiles of cost `w` each from position `start`.
+struct Block {
+    long long start;
+    int tiles, w;
+};
+__device__ __forceinline__ Block shared_block(const Line &ln, const Geometry &g, int kvh, int j) {
+    const bool pair = 2 * j + 1 < g.shared_rt;
+    return Block{kvh * ln.head + (long long)j * ln.shared_tiles * kCostPair, ln.shared_tiles,
+                 pair ? kCostPair : kCostSingle};
+}
+__device__ __forceinline__ int own_unit(const Geometry &g) {  // cost of one key tile over a sequence's row tiles
+    return (g.own_rt / 2) * kCostPair + (g.own_rt & 1) * kCostSingle;
+}
+__device__ __forceinline__ Block own_block(const Line &ln, const Geometry &g, int kvh, int cum0, int cum1, int j) {
+    const bool pair = 2 * j + 1 < g.own_rt;
+    const int tiles = cum1 - cum0;
+    return Block{kvh * ln.head + ln.shared + (long long)cum0 * own_unit(g) + (long long)j * tiles * kCostPair, tiles,
+                 pair ? kCostPair : kCostSingle};
+}
+// Tiles [i0, i1) of a block whose positions fall in [x0, x1).
+__device__ __forceinline__ void tiles_in(const Block &bl, long long x0, long long x1, int &i0, int &i1) {
+    const long long a = x0 - bl.start, b = x1 - bl.start;
+    i0 = a <= 0 ? 0 : (int)min((a + bl.w - 1) / bl.w, (long long)bl.tiles);
+    i1 = b <= 0 ? 0 : (int)min((b + bl.w - 1) / bl.w, (long long)bl.tiles);
+}
+
+// One run of key tiles of one block, as a CTA works on it.
+struct Segment {
+    int kvh, b, j;   // b = -1: shared
+    int i0, i1;      // key tiles
+    int nt;          // row tiles (1 or 2)
+    int slot;        // record
+};
+
+// Walks the segments of a CTA's share [x0, x1).
+struct Walker {
+    const Line &ln;
+    const Geometry &g;
+    const int *cum;
+    int B, cta;
+    long long pos, x1, x0;
+    __device__ Walker(const Line &l, const Geometry &ge, const int *c, int B_, int cta_, int n)
+        : ln(l), g(ge), cum(c), B(B_), cta(cta_) {
+        x0 = pos = cut(l.total, cta_, n);
+        x1 = cut(l.total, cta_ + 1, n);
+    }
+    __device__ bool next(Segment &s) {
+        while (pos < x1) {
+            const int kvh = (int)(pos / ln.head);
+            const long long rem = pos - kvh * ln.head;
+            Block bl;
+            int id;
+            s.kvh = kvh;
+            if (rem < ln.shared) {
+                s.b = -1;
+                s.j = (int)(rem / ((long long)ln.shared_tiles * kCostPair));
+                bl = shared_block(ln, g, kvh, s.j);
+                s.nt = 2 * s.j + 1 < g.shared_rt ? 2 : 1;
+                id = s.j;
+            } else {
+                const long long r2 = rem - ln.shared;
+                const int unit = (int)(r2 / own_unit(g));
+                int lo = 0, hi = B;  // the b with cum[b] <= unit < cum[b + 1]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (cum[mid] <= unit) lo = mid;
+                    else hi = mid;
+                }
+                s.b = lo;
+                const int tiles = cum[lo + 1] - cum[lo];
+                s.j = (int)((r2 - (long long)cum[lo] * own_unit(g)) / ((long long)tiles * kCostPair));
+                bl = own_block(ln, g, kvh, cum[lo], cum[lo + 1], s.j);
+                s.nt = 2 * s.j + 1 < g.own_rt ? 2 : 1;
+                id = g.shared_blocks + lo * g.own_blocks + s.j;
+            }
+            tiles_in(bl, x0, x1, s.i0, s.i1);
+            s.slot = cta + kvh * g.blocks + id;
+            pos = bl.start + (long long)bl.tiles * bl.w;
+            if (s.i0 < s.i1) return true;
+        }
+        return false;
+    }
+};
+
+template <int D>
+struct Smem {
+    static constexpr int Q_TILE = TM * D * 2;
+    static constexpr int KV_TILE = TN * D * 2;
+    static constexpr int STAGES = D == 128 ? 4 : 8;  // one K or V tile each
+    static constexpr int KV_OFF = 2 * Q_TILE;
+    static constexpr int BAR_OFF = KV_OFF + STAGES * KV_TILE;
+    // full[STAGES], empty[STAGES], q_full, q_empty, and per row tile: s_full, p_full, pv_done, o_full, o_free; fin
+    static constexpr int NBARS = 2 * STAGES + 2 + 10 + 1;
+    static constexpr int LINE_OFF = (BAR_OFF + NBARS * 8 + 63) / 64 * 64;
+    static constexpr int MISC_OFF = LINE_OFF + 64;
+    static constexpr int CUM_OFF = MISC_OFF + 16;  // int[B + 1]
+    static int alloc(int B) { return CUM_OFF + (B + 1) * 4 + 1024; }
+};
+static_assert(Smem<128>::CUM_OFF + (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024 &&
+                  Smem<64>::CUM_OFF + (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024,
+              "shared memory beyond 227 KB");
+
+// Bit i set iff key base + i lies in [a, b) (i = 0..31).
+__device__ __forceinline__ uint32_t range_bits(int a, int b, int base) {
+    const int lo = max(a - base, 0), hi = min(b - base, 32);
+    if (hi <= lo) return 0u;
+    const uint32_t below_hi = hi >= 32 ? 0xffffffffu : ((1u << hi) - 1u);
+    return below_hi & ~((1u << lo) - 1u);
+}
+
+// S = Q K^T (both K-major, 128-byte swizzle, blocks of 64 columns).
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d_s, uint64_t dq, uint64_t dk, uint32_t id) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = (uint64_t)(kk >> 2) * ((TM * 128) >> 4) + (kk & 3) * 2;
+        tc::mma_ss(d_s, dq + off, dk + off, id, kk > 0 ? 1u : 0u);
+    }
+}
+// O (+)= P V: P in TMEM (two bf16 per column), V MN-major.
+__device__ __forceinline__ void issue_pv(uint32_t d_o, uint32_t a_p, uint64_t dv, uint32_t id, bool acc) {
+#pragma unroll
+    for (int kk = 0; kk < TN / 16; ++kk) tc::mma_ts(d_o, a_p + kk * 8, dv + kk * 128, id, (acc || kk > 0) ? 1u : 0u);
+}
+
+struct Maps {
+    CUtensorMap ks, vs, kc, vc, kn, vn, q;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    shared_attn_kernel(const SharedAttnParams p, const __grid_constant__ Maps maps) {
+    using L = Smem<D>;
+    constexpr int STAGES = L::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem), sKV = sbase + L::KV_OFF, bar0 = sbase + L::BAR_OFF;
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    const uint32_t q_full = bar0 + 8u * (2 * STAGES), q_empty = q_full + 8;
+    auto s_full = [&](int t) { return q_full + 16u + 8u * t; };
+    auto p_full = [&](int t) { return q_full + 32u + 8u * t; };
+    auto pv_done = [&](int t) { return q_full + 48u + 8u * t; };
+    auto o_full = [&](int t) { return q_full + 64u + 8u * t; };
+    auto o_free = [&](int t) { return q_full + 80u + 8u * t; };
+    const uint32_t fin = q_full + 96u;
+    Line *line = reinterpret_cast<Line *>(smem + L::LINE_OFF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
+    int *cum = reinterpret_cast<int *>(smem + L::CUM_OFF);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Geometry g = geometry(p.B, p.R, p.G);
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(empty(s), 1);
+        }
+        tc::mbar_init(q_full, 1);
+        tc::mbar_init(q_empty, 1);
+        for (int t = 0; t < 2; ++t) {
+            tc::mbar_init(s_full(t), 1);
+            tc::mbar_init(p_full(t), 128);
+            tc::mbar_init(pv_done(t), 1);
+            tc::mbar_init(o_full(t), 1);
+            tc::mbar_init(o_free(t), 128);
+        }
+        tc::mbar_init(fin, 1);
+        *abort_flag = 0;
+        tc::mbar_fence_init();
+        tc::tma_prefetch_desc(&maps.ks);
+        tc::tma_prefetch_desc(&maps.vs);
+        tc::tma_prefetch_desc(&maps.kc);
+        tc::tma_prefetch_desc(&maps.vc);
+        tc::tma_prefetch_desc(&maps.kn);
+        tc::tma_prefetch_desc(&maps.vn);
+        tc::tma_prefetch_desc(&maps.q);
+    }
+    if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    // every global read below waits for the previous kernel in the stream
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    int S = p.shared_len[0];
+    if (S < 0 || S > p.S_max) S = 0;  // (combine_kernel reports it and writes nothing)
+    if (warp == 3) {  // the line: key tiles of every sequence (none where the length is out of range)
+        int sum = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int x = 0;
+            if (b < p.B) {
+                const int P = p.prefix_len[b];
+                if (P >= 0 && P <= p.P_max) x = ceil_div(P, TN) + ceil_div(p.R, TN);
+            }
+            int inc = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (b < p.B) cum[b] = sum + inc - x;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) {
+            cum[p.B] = sum;
+            line->shared_tiles = ceil_div(S, TN);
+            line->shared = (long long)line->shared_tiles * ((g.shared_rt / 2) * kCostPair + (g.shared_rt & 1) * kCostSingle);
+            line->head = line->shared + (long long)sum * own_unit(g);
+            line->total = line->head * p.Hkv;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const Line ln = *line;
+    if (blockIdx.x == 0) {  // for combine_kernel
+        if (tid == 0) *reinterpret_cast<Line *>(p.ws) = ln;
+        for (int b = tid; b <= p.B; b += THREADS) reinterpret_cast<int *>(p.ws + kLineBytes)[b] = cum[b];
+    }
+    const uint32_t tbase = *tmem_slot;
+    const int cta = blockIdx.x, ncta = gridDim.x;
+    const long long wl = kWaitCycles;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+        Walker walk(ln, g, cum, p.B, cta, ncta);
+        Segment sg;
+        if (warp == 0 && lane == 0) {
+            // ================= K/V producer =================
+            int it = 0;
+            bool ok = true;
+            while (ok && walk.next(sg)) {
+                const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
+                const int TP = ceil_div(P, TN), np = ceil_div(P, BOXR);
+                const int32_t *pages = sg.b < 0 ? p.shared_table : p.block_table + (size_t)sg.b * p.max_pages;
+                for (int i = sg.i0; i < sg.i1 && ok; ++i) {
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v, ++it) {
+                        const int st = it % STAGES;
+                        if (it >= STAGES && !tc::mbar_wait(empty(st), (it / STAGES - 1) & 1, abort_flag, wl)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = full(st), dst = sKV + st * L::KV_TILE;
+                        tc::mbar_arrive_expect_tx(bar, L::KV_TILE);
+                        if (i >= TP) {  // new keys
+                            const int z = sg.b * p.R + (i - TP) * TN;
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                tc::tma_load_3d(dst + h * TN * 128, v ? &maps.vn : &maps.kn, h * 64, sg.kvh, z, bar);
+                        } else if (p.block_table) {  // two pages
+                            // (the second box of a tile that ends within its first page re-reads that page: rows past
+                            // the end are excluded below; a page id out of range reads page 0 and is reported, and its
+                            // rows dropped, by combine_kernel)
+                            for (int h2 = 0; h2 < 2; ++h2) {
+                                const int pi = min(2 * i + h2, np - 1);
+                                int pg = __ldg(pages + pi);
+                                if (pg < 0 || pg >= p.num_pages) pg = 0;
+                                const int y = (pg * p.Hkv + sg.kvh) * BOXR;
+#pragma unroll
+                                for (int h = 0; h < D / 64; ++h)
+                                    tc::tma_load_2d(dst + h * TN * 128 + h2 * BOXR * 128, v ? &maps.vc : &maps.kc,
+                                                    h * 64, y, bar);
+                            }
+                        } else {
+                            const int y = (sg.b < 0 ? sg.kvh * p.S_max : (sg.b * p.Hkv + sg.kvh) * p.P_max) + i * TN;
+                            const CUtensorMap *m = sg.b < 0 ? (v ? &maps.vs : &maps.ks) : (v ? &maps.vc : &maps.kc);
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h) tc::tma_load_2d(dst + h * TN * 128, m, h * 64, y, bar);
+                        }
+                    }
+                }
+            }
+            // nothing may land after the CTA exits: only the last copy of each stage can still be in flight
+            for (int i = max(0, it - STAGES); i < it; ++i)
+                tc::mbar_wait_drain(full(i % STAGES), (i / STAGES) & 1, wl);
+        } else if (warp == 2 && lane == 0) {
+            // ================= Q producer =================
+            const uint32_t bytes = (uint32_t)D * p.G * g.RT * 2;
+            int n = 0;
+            while (walk.next(sg)) {
+                if (n > 0 && !tc::mbar_wait(q_empty, (n - 1) & 1, abort_flag, wl)) break;
+                tc::mbar_arrive_expect_tx(q_full, sg.nt * bytes);
+                for (int t = 0; t < sg.nt; ++t) {
+                    const int z = (sg.b < 0 ? 0 : sg.b * p.R) + (2 * sg.j + t) * g.RT;
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        tc::tma_load_3d(sbase + t * L::Q_TILE + h * TM * 128, &maps.q, h * 64, sg.kvh * p.G, z, q_full);
+                }
+                ++n;
+            }
+            if (n > 0) tc::mbar_wait_drain(q_full, (n - 1) & 1, wl);
+        } else if (warp == 1 && lane == 0) {
+            // ================= MMA issue =================
+            constexpr uint32_t id_qk = tc::idesc_bf16_f32(TM, TN, 0, 0), id_pv = tc::idesc_bf16_f32(TM, D, 0, 1);
+            const uint64_t dq = tc::smem_desc_sw128(sbase, 16, 1024);
+            const uint64_t dk = tc::smem_desc_sw128(sKV, 16, 1024);
+            const uint64_t dv = tc::smem_desc_sw128(sKV, TN * 128, 1024);
+            constexpr uint64_t kQ = L::Q_TILE >> 4, kS = L::KV_TILE >> 4;
+            int it = 0, n = 0;
+            int np[2] = {0, 0}, npv[2] = {0, 0}, ns[2] = {0, 0};  // P tiles, PVs waited for, segments of each row tile
+            bool ok = true;
+            // (pv_done(t) is waited for once per PV, in order)
+            auto wait_pv = [&](int t) { return tc::mbar_wait(pv_done(t), npv[t]++ & 1, abort_flag, wl); };
+            auto wait_full = [&](int i) { return tc::mbar_wait(full(i % STAGES), (i / STAGES) & 1, abort_flag, wl); };
+            while (ok && walk.next(sg)) {
+                const int nt = sg.nt, nk = sg.i1 - sg.i0;
+                ok = tc::mbar_wait(q_full, n & 1, abort_flag, wl) && wait_full(it);
+                ++n;
+                for (int t = 0; t < nt && ok; ++t) {
+                    if (ns[t] > 0) ok = wait_pv(t);  // the last segment's PV has read its P
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    issue_qk<D>(tbase + t * 128, dq + t * kQ, dk + (it % STAGES) * kS, id_qk);
+                    tc::mma_commit(s_full(t));
+                }
+                if (!ok) break;
+                tc::mma_commit(empty(it % STAGES));
+                if (nk == 1) tc::mma_commit(q_empty);
+                for (int i = 0; i < nk && ok; ++i, it += 2) {
+                    const int vst = (it + 1) % STAGES, kst = (it + 2) % STAGES;
+                    const bool more = i + 1 < nk;
+                    for (int t = 0; t < nt && ok; ++t) {
+                        if (t == 0) ok = wait_full(it + 1);
+                        if (ok && i == 0 && ns[t] > 0) ok = tc::mbar_wait(o_free(t), (ns[t] - 1) & 1, abort_flag, wl);
+                        ok = ok && tc::mbar_wait(p_full(t), np[t]++ & 1, abort_flag, wl);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        issue_pv(tbase + 256 + t * D, tbase + t * 128, dv + vst * kS, id_pv, i > 0);
+                        tc::mma_commit(pv_done(t));
+                        if (!more) tc::mma_commit(o_full(t));
+                        if (t == nt - 1) tc::mma_commit(empty(vst));
+                        if (more) {
+                            if (t == 0) ok = wait_full(it + 2);
+                            ok = ok && wait_pv(t);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            issue_qk<D>(tbase + t * 128, dq + t * kQ, dk + kst * kS, id_qk);
+                            tc::mma_commit(s_full(t));
+                            if (t == nt - 1) {
+                                tc::mma_commit(empty(kst));
+                                if (i + 2 == nk) tc::mma_commit(q_empty);
+                            }
+                        }
+                    }
+                }
+                for (int t = 0; t < nt; ++t) ++ns[t];
+            }
+            tc::mma_commit(fin);  // every MMA completes before TMEM is freed
+            tc::mbar_wait_drain(fin, 0, wl);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        // ================= softmax: warpgroup t has row tile t =================
+        const int t = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+        const int rr = row / p.G;  // row (b, r) within the tile
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const uint32_t s_col = tbase + lane_off + t * 128, o_col = tbase + lane_off + 256 + t * D;
+        const float sl2 = p.scale_log2;
+        Walker walk(ln, g, cum, p.B, cta, ncta);
+        Segment sg;
+        int ring = 0, n_s = 0, n_seg = 0;
+        bool ok = true;
+        while (walk.next(sg)) {
+            const int nk = sg.i1 - sg.i0, ring0 = ring;
+            ring += 2 * nk;
+            if (t >= sg.nt) continue;
+            const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
+            const int TP = ceil_div(P, TN);
+            const int r = (2 * sg.j + t) * g.RT + rr;  // row of the sequence, or of the batch (shared)
+            const bool valid = rr < g.RT && r < (sg.b < 0 ? p.B * p.R : p.R);
+            const bool work = __any_sync(0xffffffffu, valid);
+            // visible new keys of row r: [0, vis_lim) and [vis_glo, vis_ghi)
+            int vis_lim = r + 1, vis_glo = 0, vis_ghi = 0;
+            if (p.mask_mode == TIDAR_MASK_HYBRID && r >= p.k) {
+                const int grp = (r - p.k) / p.k;
+                vis_lim = grp;
+                vis_glo = p.k + grp * p.k;
+                vis_ghi = vis_glo + p.k;
+            }
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int i = 0; i < nk; ++i, ++n_s) {
+                const int kt = sg.i0 + i;
+                bool have = ok && tc::mbar_wait(s_full(t), n_s & 1, abort_flag, wl);
+                ok = __all_sync(0xffffffffu, have);  // TMEM accesses are warp-collective
+                if (!ok) break;
+                const int keys = kt < TP ? min(TN, P - kt * TN) : min(TN, p.R - (kt - TP) * TN);
+                if (work) {
+                    tc::fence_after_sync();
+                    uint32_t u[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, u[c]);
+                    tc::tmem_wait_ld();
+                    if (kt >= TP || keys < TN) {  // by select, so that masked scores may be anything
+                        int lo = keys, glo = 0, ghi = 0;
+                        if (kt >= TP) {
+                            const int nn0 = (kt - TP) * TN;
+                            lo = min(vis_lim - nn0, keys);
+                            glo = vis_glo - nn0;
+                            ghi = min(vis_ghi - nn0, keys);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t bits = range_bits(0, lo, c * 32) | range_bits(glo, ghi, c * 32);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) u[c][j] = (bits >> j) & 1u ? u[c][j] : 0xff800000u;
+                        }
+                    }
+                    float m8[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) m8[j] = __uint_as_float(u[0][j]);
+#pragma unroll
+                    for (int j = 8; j < 128; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(u[j >> 5][j & 31]));
+                    const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * sl2;
+                    // the running max is raised only when it grows by more than 2^8: a stale one is exact as long as
+                    // the weights fit, and O is rarely rescaled
+                    const bool grow = mx > m_run + 8.f || (m_run == -INFINITY && mx > -INFINITY);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow && m_run > -INFINITY ? fast_exp2(m_run - mx) : 1.f;
+                        if (i > 0 && __any_sync(0xffffffffu, f < 1.f)) {
+                            // (S of this tile is complete, so PV of the last one is, and the next awaits this P)
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t v[32];
+                                tc::tmem_ld32(o_col + c * 32, v);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                                tc::tmem_st32(o_col + c * 32, v);
+                            }
+                        }
+                        if (grow) {
+                            l_run *= f;
+                            m_run = mx;
+                        }
+                    }
+                    const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                    float s8[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s8[j] = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float a = fast_exp2(fmaf(__uint_as_float(u[2 * h + (j >> 4)][(2 * j) & 31]), sl2, neg_m));
+                            const float e =
+                                fast_exp2(fmaf(__uint_as_float(u[2 * h + (j >> 4)][(2 * j + 1) & 31]), sl2, neg_m));
+                            s8[(2 * j) & 7] += a;
+                            s8[(2 * j + 1) & 7] += e;
+                            pk[j] = pack_bf16x2(a, e);
+                        }
+                        tc::tmem_st32(s_col + h * 32, pk);
+                    }
+                    l_run += ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
+                }
+                if (t == 0 && keys < TN) {
+                    // keys past the end: zero their V rows (0 * garbage could be NaN) before any PV reads them
+                    const int vi = ring0 + 2 * i + 1, st = vi % STAGES;
+                    const bool got = tc::mbar_wait(full(st), (vi / STAGES) & 1, abort_flag, wl);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    uint8_t *vrow = smem + L::KV_OFF + st * L::KV_TILE;
+                    for (int idx = row; idx < (TN - keys) * (D / 8); idx += 128) {
+                        const int j = keys + idx / (D / 8), c = idx % (D / 8);
+                        *reinterpret_cast<uint4 *>(vrow + (c >> 3) * TN * 128 + j * 128 + ((c & 7) << 4)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_proxy_async_smem();
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(p_full(t));
+            }
+            tc::tmem_wait_st();
+            // ---- the record: the row over its largest magnitude as fp16 (|error| <= 2^-12 of it) and an fp32 scale ----
+            bool got = ok && tc::mbar_wait(o_full(t), n_seg & 1, abort_flag, wl);
+            ok = __all_sync(0xffffffffu, got);
+            if (!ok) break;
+            ++n_seg;
+            if (work) {
+                tc::fence_after_sync();
+                uint32_t v[D / 32][32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) tc::tmem_ld32(o_col + c * 32, v[c]);
+                tc::tmem_wait_ld();
+                float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < D; ++j) a4[j & 3] = fmaxf(a4[j & 3], fabsf(__uint_as_float(v[j >> 5][j & 31])));
+                const float amax = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
+                const float rs = amax > 0.f ? __fdividef(1.f, amax) : 0.f;
+                if (valid) {
+                    uint8_t *rec = p.ws + info_bytes(p.B) + ((size_t)sg.slot * 2 + t) * tile_record_bytes(D);
+                    uint4 *vals = reinterpret_cast<uint4 *>(rec) + row;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[c >> 2][(c & 3) * 8 + e]) * rs;
+                        vals[c * TM] = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
+                                                  pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                    }
+                    reinterpret_cast<float2 *>(rec + TM * D * 2)[row] =
+                        make_float2(l_run == 0.f ? -INFINITY : m_run + __log2f(l_run),  // (a NaN sum stays one)
+                                    l_run == 0.f ? 0.f : amax / l_run);
+                }
+            }
+            tc::fence_before_sync();
+            tc::mbar_arrive(o_free(t));
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tbase, 512);
+    }
+    if (tid == 0 && *abort_flag) atomicOr(p.dev_status, TIDAR_DEV_TIMEOUT);
+}
+
+// Joins the records of 32 rows (lane = row) of one KV head; warp w has columns [8w, 8w + 8).  Also reports lengths and
+// pages out of range and leaves those rows alone.
+template <int D>
+__global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p, int ncta) {
+    __shared__ int bad_seq[32];
+    const int lane = threadIdx.x & 31, chunk = threadIdx.x >> 5;
+    const int kvh = blockIdx.y;
+    const long rows = (long)p.B * p.R * p.G;
+    const long m = (long)blockIdx.x * 32 + lane;
+    const Geometry g = geometry(p.B, p.R, p.G);
+    const int per_seq = p.R * p.G;
+    const int b = (int)min(m / per_seq, (long)p.B - 1);
+    const int mr = (int)(m - (long)b * per_seq), r = mr / p.G, gq = mr - r * p.G;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int S = p.shared_len[0], P = p.prefix_len[b];
-    if (S < 0 || S > p.S_max || P < 0 || P > p.P_max) {
-        if (lane == 0) atomicOr(p.dev_status, TIDAR_DEV_BAD_PREFIX);
+    int bits = (S < 0 || S > p.S_max || P < 0 || P > p.P_max) ? TIDAR_DEV_BAD_PREFIX : 0;
+    if (p.block_table) {
+        const bool s_ok = S >= 0 && S <= p.S_max;
+        if (s_ok && block_bad_page(p.shared_table, S, p.num_pages)) bits |= TIDAR_DEV_BAD_PAGE;
+        if (threadIdx.x < 32) bad_seq[lane] = 0;
+        __syncthreads();
+        // (at most 32 rows: the sequences of the block's first to last row)
+        const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 31);
+        for (int s = b0; s <= b1; ++s) {
+            const int n = p.prefix_len[s];
+            if (n < 0 || n > p.P_max) continue;
+            for (int i = threadIdx.x; i < ceil_div(n, kPageRows); i += blockDim.x) {
+                const int pg = p.block_table[(size_t)s * p.max_pages + i];
+                if (pg < 0 || pg >= p.num_pages) bad_seq[s - b0] = 1;
+            }
+        }
+        __syncthreads();
+        if (bad_seq[b - b0]) bits |= TIDAR_DEV_BAD_PAGE;
+    }
+    if (m >= rows) return;
+    if (bits) {
+        if (chunk == 0) atomicOr(p.dev_status, bits);
         return;
     }
-    if (p.block_table) {
-        bool bad = false;
-        for (int i = lane; i < ceil_div(S, kPageRows); i += 32)
-            bad |= p.shared_table[i] < 0 || p.shared_table[i] >= p.num_pages;
-        for (int i = lane; i < ceil_div(P, kPageRows); i += 32) {
-            const int pg = p.block_table[(size_t)b * p.max_pages + i];
-            bad |= pg < 0 || pg >= p.num_pages;
+    const Line ln = *reinterpret_cast<const Line *>(p.ws);
+    const int *cum = reinterpret_cast<const int *>(p.ws + kLineBytes);
+    const uint8_t *recs = p.ws + info_bytes(p.B);
+    // the two blocks that hold this row: shared (x = 0) and own (x = 1)
+    const int sr = b * p.R + r, st = sr / g.RT, ot = r / g.RT;
+    Block bl[2] = {shared_block(ln, g, kvh, st / 2), own_block(ln, g, kvh, cum[b], cum[b + 1], ot / 2)};
+    const int id[2] = {kvh * g.blocks + st / 2, kvh * g.blocks + g.shared_blocks + b * g.own_blocks + ot / 2};
+    const int tile[2] = {st & 1, ot & 1};
+    const int row[2] = {(sr - st * g.RT) * p.G + gq, (r - ot * g.RT) * p.G + gq};
+    float mx = -INFINITY;
+    // every record of the row, in the order of the line
+    auto each = [&](auto &&f) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (bl[x].tiles == 0) continue;
+            const int c0 = (int)(bl[x].start * ncta / ln.total);
+            const int c1 = (int)((bl[x].start + (long long)(bl[x].tiles - 1) * bl[x].w) * ncta / ln.total);
+            for (int c = c0; c <= c1; ++c) {
+                int i0, i1;
+                tiles_in(bl[x], cut(ln.total, c, ncta), cut(ln.total, c + 1, ncta), i0, i1);
+                if (i0 < i1) f(recs + ((size_t)(c + id[x]) * 2 + tile[x]) * tile_record_bytes(D), row[x]);
+            }
         }
-        if (__any_sync(0xffffffffu, bad)) {
-            if (lane == 0) atomicOr(p.dev_status, TIDAR_DEV_BAD_PAGE);
-            return;
+    };
+    each([&](const uint8_t *rec, int rw) {
+        mx = fmaxf(mx, reinterpret_cast<const float2 *>(rec + TM * D * 2)[rw].x);
+    });
+    float acc[8], wsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    each([&](const uint8_t *rec, int rw) {
+        const float2 hd = reinterpret_cast<const float2 *>(rec + TM * D * 2)[rw];
+        const uint4 raw = reinterpret_cast<const uint4 *>(rec)[chunk * TM + rw];
+        const float w = hd.x == -INFINITY ? 0.f : fast_exp2(hd.x - mx);
+        wsum += w;
+        const float f = w * hd.y;
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = unpack_half2(u[e]);
+            acc[2 * e] = fmaf(f, v.x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(f, v.y, acc[2 * e + 1]);
         }
-    }
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-    for (int e = 0; e < per; ++e) q[e] = __bfloat162float(p.q[row * p.D + lane * per + e]);
-    for (int n = 0; n < S + P + p.R; ++n) {
-        const bf16 *kr, *vr;
-        if (n >= S + P) {
-            const int nn = n - S - P;
-            if (!new_key_visible(p.mask_mode, p.k, r, nn)) continue;
-            const size_t at = ((size_t)(b * p.R + nn) * p.Hkv + kvh) * p.D;
-            kr = p.k_new + at;
-            vr = p.v_new + at;
-        } else if (p.block_table) {
-            const int i = n < S ? n : n - S;
-            const int pg = n < S ? p.shared_table[i / kPageRows] : p.block_table[(size_t)b * p.max_pages + i / kPageRows];
-            const size_t at = (((size_t)pg * p.Hkv + kvh) * kPageRows + i % kPageRows) * p.D;
-            kr = p.k_cache + at;
-            vr = p.v_cache + at;
-        } else if (n < S) {
-            const size_t at = ((size_t)kvh * p.S_max + n) * p.D;
-            kr = p.k_shared + at;
-            vr = p.v_shared + at;
-        } else {
-            const size_t at = (((size_t)b * p.Hkv + kvh) * p.P_max + (n - S)) * p.D;
-            kr = p.k_cache + at;
-            vr = p.v_cache + at;
-        }
-        float s = 0.f;
-        for (int e = 0; e < per; ++e) s = fmaf(q[e], __bfloat162float(kr[lane * per + e]), s);
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-        l = l * f + w;
-        for (int e = 0; e < per; ++e) o[e] = o[e] * f + w * __bfloat162float(vr[lane * per + e]);
-        m = mn;
-    }
-    for (int e = 0; e < per; ++e) p.out[row * p.D + lane * per + e] = __float2bfloat16_rn(o[e] / l);
-    if (lane == 0 && p.lse) p.lse[row] = (m + log2f(l)) * kLn2;
+    });
+    const float inv = 1.f / wsum;
+    const size_t orow = ((size_t)b * p.R + r) * p.Hq + kvh * p.G + gq;
+    *reinterpret_cast<uint4 *>(p.out + orow * D + chunk * 8) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (chunk == 0 && p.lse) p.lse[orow] = (mx + __log2f(wsum)) * kLn2;
+}
+
+// ---- host side ---------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (EncodeTiledFn) nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// bf16, 128-byte swizzle; dims and box innermost first, rows packed.
+bool map_2d(CUtensorMap *m, const void *base, int D, long long rows, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_3d(CUtensorMap *m, const void *base, int D, int heads, long long rows, int box_heads, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * heads};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
+    Maps mp;
+    if (!encode_fn()) return cudaErrorNotSupported;
+    const bool paged = p.block_table != nullptr;
+    // (an empty part has no map of its own: no tile of it is ever loaded)
+    const bool no_shared = p.S_max == 0, no_own = p.P_max == 0;
+    const long long pool_rows = (long long)p.num_pages * p.Hkv * kPageRows;
+    const long long s_rows = no_shared ? 1 : (long long)p.Hkv * p.S_max;
+    const long long o_rows = no_own ? 1 : (long long)p.B * p.Hkv * p.P_max;
+    const int box = paged ? BOXR : TN;
+    if (!map_2d(&mp.ks, paged || !no_shared ? p.k_shared : p.q, D, paged ? pool_rows : s_rows, box) ||
+        !map_2d(&mp.vs, paged || !no_shared ? p.v_shared : p.q, D, paged ? pool_rows : s_rows, box) ||
+        !map_2d(&mp.kc, paged || !no_own ? p.k_cache : p.q, D, paged ? pool_rows : o_rows, box) ||
+        !map_2d(&mp.vc, paged || !no_own ? p.v_cache : p.q, D, paged ? pool_rows : o_rows, box) ||
+        !map_3d(&mp.kn, p.k_new, D, p.Hkv, (long long)p.B * p.R, 1, TN) ||
+        !map_3d(&mp.vn, p.v_new, D, p.Hkv, (long long)p.B * p.R, 1, TN) ||
+        !map_3d(&mp.q, p.q, D, p.Hq, (long long)p.B * p.R, p.G, rows_per_tile(p.G)))
+        return cudaErrorInvalidValue;
+    const int smem = Smem<D>::alloc(p.B);
+    cudaError_t e = cudaFuncSetAttribute(shared_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kNumSMs, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, shared_attn_kernel<D>, p, mp);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.R * p.G + 31) / 32), p.Hkv, 1);
+    cfg.blockDim = dim3(D * 4, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, kNumSMs);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t shared_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+size_t shared_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int R, int, int) {
+    const Geometry g = geometry(B, R, Hq / Hkv);
+    // a segment's record is at cta + block: along the line both only grow, and one of them from segment to segment
+    return info_bytes(B) + ((size_t)kNumSMs + (size_t)Hkv * g.blocks) * 2 * tile_record_bytes(D);
+}
 
 cudaError_t shared_attn_launch(const SharedAttnParams &p, cudaStream_t s) {
-    const long rows = (long)p.B * p.R * p.Hq;
-    shared_attn_rows_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
 }
 
 }  // namespace tidar
