@@ -13,11 +13,20 @@
 // partial record; combine_kernel joins a row's records in a fixed order.  The line and its cuts follow from the lengths
 // alone, which every CTA reads on the device, so nothing waits on the host and nothing on timing.
 //
-// A CTA (12 warps): warp 0 streams K and V tiles by TMA through one ring; warp 2 loads Q; warp 1 issues every MMA;
-// warps 4-7 and 8-11 are the softmax of row tile 0 and 1 (thread = row = TMEM lane).  The two row tiles share each K/V
-// tile and run half a period apart: while one's softmax works, the tensor cores multiply for the other.
-// TMEM: S0 [0, 128), S1 [128, 256), O0 [256, 256 + D), O1 [256 + D, 256 + 2D).  P (bf16) overwrites the first 64 columns
-// of its S, so S = Q K of the next key tile is issued once the PV that reads P has completed.
+// A CTA (12 warps): warp 0 streams K and V tiles by TMA through one ring; warp 2 walks the line, hands out the segments
+// and loads Q; warps 1 and 3 issue the MMAs of row tile 0 and 1; warps 4-7 and 8-11 are the softmax of row tile 0 and 1
+// (thread = row = TMEM lane).  The two row tiles share each K/V tile and are independent otherwise, so the tensor cores
+// multiply for one while the other exponentiates.
+// A key tile is taken in halves of 64 keys.  TMEM: S of row tile t in two buffers [128t, 128t + 64) and [128t + 64,
+// 128t + 128), O at [256 + D t, 256 + D t + D); P (bf16) overwrites the first 32 columns of its S.  S of half u + 2 is
+// issued once the PV of half u, the last reader of that buffer, has completed, while the softmax works on half u + 1:
+// the round trip P -> PV -> next S is off its path.  (Whole tiles of 128 keys in one buffer each, as TMEM holds no more
+// at D = 128, left the softmax waiting 2,240 of 4,395 cycles per tile on that round trip.)
+//
+// The exponentials bound the softmax (a warp-wide ex2 takes ~9 cycles of its sub-partition's MUFU): a quarter of them
+// is taken by a polynomial on the FMA pipe, and scaling and sums use the packed fp32 pair instructions.  128 values per
+// thread, two warps per sub-partition, measured alone: 2,497 cycles, packed 2,269, with the quarter 1,903, with a half
+// 1,999.
 #include "cache_ops.cuh"
 #include "tc.cuh"
 
@@ -27,25 +36,28 @@ namespace {
 
 constexpr int TM = 128;
 constexpr int TN = 128;
+constexpr int TH = 64;  // keys of half a tile
 constexpr int THREADS = 384;
 constexpr int BOXR = kPageRows;
-// Cost of one key tile for a block of two row tiles and of one.
+// Cost of one key tile for a block of two row tiles and of one (where every CTA has a few tiles; see Line).
 constexpr int kCostPair = 3, kCostSingle = 2;
 constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
 
-// What the line of key tiles is made of; CTA 0 leaves it in the workspace for combine_kernel, followed by cum[0..B]:
-// cum[b] = key tiles of the sequences before b.
+// The line of key tiles (cum[b], beside it: key tiles of the sequences before b).  Every CTA's share is at least the
+// cost of one tile, so the CTAs from a block's first tile to its last all have a part of it: where there are fewer
+// tiles than CTAs every tile costs 1 and that many CTAs work.
 struct Line {
     long long total;   // cost of all KV heads
     long long head;    // cost of one KV head
     long long shared;  // of its shared blocks
     int shared_tiles;  // key tiles of the shared prefix
-    int pad;
+    int pair, single;  // cost of a key tile for two row tiles, for one
+    int ncta;          // CTAs that work
 };
-constexpr int kLineBytes = 256;
 
 __host__ __device__ __forceinline__ int rows_per_tile(int G) { return TM / G; }
-__host__ __device__ __forceinline__ size_t info_bytes(int B) { return align256(kLineBytes + (size_t)(B + 1) * 4); }
+// The workspace: (first, last) CTA of every block, then the records.
+__host__ __device__ __forceinline__ size_t info_bytes(size_t blocks) { return align256(blocks * 8); }
 // One record: two row tiles, each [D/8 chunks][128 rows] 16-byte chunks of 8 fp16 and a header [128 rows] (log2 of the
 // row's sum, scale of its values).
 __host__ __device__ __forceinline__ size_t tile_record_bytes(int D) { return (size_t)TM * (D * 2 + 8); }
@@ -74,17 +86,15 @@ struct Block {
 };
 __device__ __forceinline__ Block shared_block(const Line &ln, const Geometry &g, int kvh, int j) {
     const bool pair = 2 * j + 1 < g.shared_rt;
-    return Block{kvh * ln.head + (long long)j * ln.shared_tiles * kCostPair, ln.shared_tiles,
-                 pair ? kCostPair : kCostSingle};
+    return Block{kvh * ln.head + (long long)j * ln.shared_tiles * ln.pair, ln.shared_tiles, pair ? ln.pair : ln.single};
 }
-__device__ __forceinline__ int own_unit(const Geometry &g) {  // cost of one key tile over a sequence's row tiles
-    return (g.own_rt / 2) * kCostPair + (g.own_rt & 1) * kCostSingle;
-}
+// cost of one key tile over n row tiles
+__device__ __forceinline__ int unit(const Line &ln, int n) { return (n / 2) * ln.pair + (n & 1) * ln.single; }
 __device__ __forceinline__ Block own_block(const Line &ln, const Geometry &g, int kvh, int cum0, int cum1, int j) {
     const bool pair = 2 * j + 1 < g.own_rt;
     const int tiles = cum1 - cum0;
-    return Block{kvh * ln.head + ln.shared + (long long)cum0 * own_unit(g) + (long long)j * tiles * kCostPair, tiles,
-                 pair ? kCostPair : kCostSingle};
+    return Block{kvh * ln.head + ln.shared + (long long)cum0 * unit(ln, g.own_rt) + (long long)j * tiles * ln.pair, tiles,
+                 pair ? ln.pair : ln.single};
 }
 // Tiles [i0, i1) of a block whose positions fall in [x0, x1).
 __device__ __forceinline__ void tiles_in(const Block &bl, long long x0, long long x1, int &i0, int &i1) {
@@ -94,11 +104,13 @@ __device__ __forceinline__ void tiles_in(const Block &bl, long long x0, long lon
 }
 
 // One run of key tiles of one block, as a CTA works on it.
-struct Segment {
-    int kvh, b, j;   // b = -1: shared
+struct __align__(16) Segment {
+    int kvh, b;      // b = -1: shared
     int i0, i1;      // key tiles
-    int nt;          // row tiles (1 or 2)
-    int slot;        // record
+    int row0;        // first row (of the sequence, or of the batch) of the block's first row tile
+    int nt;          // row tiles (1 or 2; 0: no more segments)
+    int id;          // block
+    int last;        // the run ends the block
 };
 
 // Walks the segments of a CTA's share [x0, x1).
@@ -108,10 +120,10 @@ struct Walker {
     const int *cum;
     int B, cta;
     long long pos, x1, x0;
-    __device__ Walker(const Line &l, const Geometry &ge, const int *c, int B_, int cta_, int n)
+    __device__ Walker(const Line &l, const Geometry &ge, const int *c, int B_, int cta_)
         : ln(l), g(ge), cum(c), B(B_), cta(cta_) {
-        x0 = pos = cut(l.total, cta_, n);
-        x1 = cut(l.total, cta_ + 1, n);
+        x0 = pos = cta < l.ncta ? cut(l.total, cta_, l.ncta) : 0;
+        x1 = cta < l.ncta ? cut(l.total, cta_ + 1, l.ncta) : 0;
     }
     __device__ bool next(Segment &s) {
         while (pos < x1) {
@@ -122,34 +134,40 @@ struct Walker {
             s.kvh = kvh;
             if (rem < ln.shared) {
                 s.b = -1;
-                s.j = (int)(rem / ((long long)ln.shared_tiles * kCostPair));
-                bl = shared_block(ln, g, kvh, s.j);
-                s.nt = 2 * s.j + 1 < g.shared_rt ? 2 : 1;
-                id = s.j;
+                const int j = (int)(rem / ((long long)ln.shared_tiles * ln.pair));
+                bl = shared_block(ln, g, kvh, j);
+                s.nt = 2 * j + 1 < g.shared_rt ? 2 : 1;
+                s.row0 = 2 * j * g.RT;
+                id = j;
             } else {
                 const long long r2 = rem - ln.shared;
-                const int unit = (int)(r2 / own_unit(g));
-                int lo = 0, hi = B;  // the b with cum[b] <= unit < cum[b + 1]
+                const int ou = unit(ln, g.own_rt), at = (int)(r2 / ou);
+                int lo = 0, hi = B;  // the b with cum[b] <= at < cum[b + 1]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (cum[mid] <= unit) lo = mid;
+                    if (cum[mid] <= at) lo = mid;
                     else hi = mid;
                 }
                 s.b = lo;
                 const int tiles = cum[lo + 1] - cum[lo];
-                s.j = (int)((r2 - (long long)cum[lo] * own_unit(g)) / ((long long)tiles * kCostPair));
-                bl = own_block(ln, g, kvh, cum[lo], cum[lo + 1], s.j);
-                s.nt = 2 * s.j + 1 < g.own_rt ? 2 : 1;
-                id = g.shared_blocks + lo * g.own_blocks + s.j;
+                const int j = (int)((r2 - (long long)cum[lo] * ou) / ((long long)tiles * ln.pair));
+                bl = own_block(ln, g, kvh, cum[lo], cum[lo + 1], j);
+                s.nt = 2 * j + 1 < g.own_rt ? 2 : 1;
+                s.row0 = 2 * j * g.RT;
+                id = g.shared_blocks + lo * g.own_blocks + j;
             }
             tiles_in(bl, x0, x1, s.i0, s.i1);
-            s.slot = cta + kvh * g.blocks + id;
+            s.id = kvh * g.blocks + id;
+            s.last = s.i1 == bl.tiles;
             pos = bl.start + (long long)bl.tiles * bl.w;
             if (s.i0 < s.i1) return true;
         }
+        s.nt = 0;
         return false;
     }
 };
+constexpr int SEGS = 4;                // segments the scheduler keeps ahead
+constexpr int kSegReaders = 3 + 8;     // the K/V and MMA warps and the softmax warps
 
 template <int D>
 struct Smem {
@@ -158,16 +176,26 @@ struct Smem {
     static constexpr int STAGES = D == 128 ? 4 : 8;  // one K or V tile each
     static constexpr int KV_OFF = 2 * Q_TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * KV_TILE;
-    // full[STAGES], empty[STAGES], q_full, q_empty, and per row tile: s_full, p_full, pv_done, o_full, o_free; fin
-    static constexpr int NBARS = 2 * STAGES + 2 + 10 + 1;
-    static constexpr int LINE_OFF = (BAR_OFF + NBARS * 8 + 63) / 64 * 64;
+    // full[STAGES], empty[STAGES], q_full, q_empty, per row tile and S buffer s_full, p_full, pv_done, per row tile
+    // o_full, o_free, per MMA issuer fin; seg_full[SEGS], seg_empty[SEGS]
+    static constexpr int NBARS = 2 * STAGES + 2 + 12 + 8 + 2 * SEGS;
+    static constexpr int SEG_OFF = (BAR_OFF + NBARS * 8 + 63) / 64 * 64;
+    static constexpr int LINE_OFF = SEG_OFF + SEGS * (int)sizeof(Segment);
     static constexpr int MISC_OFF = LINE_OFF + 64;
     static constexpr int CUM_OFF = MISC_OFF + 16;  // int[B + 1]
     static int alloc(int B) { return CUM_OFF + (B + 1) * 4 + 1024; }
 };
+static_assert(sizeof(Line) <= 64, "the line's place in shared memory");
 static_assert(Smem<128>::CUM_OFF + (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024 &&
                   Smem<64>::CUM_OFF + (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024,
               "shared memory beyond 227 KB");
+
+// One lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(one));
+    return one != 0;
+}
 
 // Bit i set iff key base + i lies in [a, b) (i = 0..31).
 __device__ __forceinline__ uint32_t range_bits(int a, int b, int base) {
@@ -177,7 +205,7 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b, int base) {
     return below_hi & ~((1u << lo) - 1u);
 }
 
-// S = Q K^T (both K-major, 128-byte swizzle, blocks of 64 columns).
+// S = Q K^T over 64 keys (both K-major, 128-byte swizzle, blocks of 64 columns).
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t d_s, uint64_t dq, uint64_t dk, uint32_t id) {
 #pragma unroll
@@ -186,10 +214,103 @@ __device__ __forceinline__ void issue_qk(uint32_t d_s, uint64_t dq, uint64_t dk,
         tc::mma_ss(d_s, dq + off, dk + off, id, kk > 0 ? 1u : 0u);
     }
 }
-// O (+)= P V: P in TMEM (two bf16 per column), V MN-major.
+// O (+)= P V over 64 keys: P in TMEM (two bf16 per column), V MN-major.
 __device__ __forceinline__ void issue_pv(uint32_t d_o, uint32_t a_p, uint64_t dv, uint32_t id, bool acc) {
 #pragma unroll
-    for (int kk = 0; kk < TN / 16; ++kk) tc::mma_ts(d_o, a_p + kk * 8, dv + kk * 128, id, (acc || kk > 0) ? 1u : 0u);
+    for (int kk = 0; kk < TH / 16; ++kk) tc::mma_ts(d_o, a_p + kk * 8, dv + kk * 128, id, (acc || kk > 0) ? 1u : 0u);
+}
+
+// Pairs of fp32 in one 64-bit register (the packed instructions round each half as the scalar ones do).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The greater of three; NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x of both halves on the FMA pipe (below -126: 2^-126; from 128, and NaN: infinite or out of range): x = n + f, n the nearest integer (by adding and
+// taking away 1.5 2^23), 2^f by the quartic of least relative error on [-1/2, 1/2] (2.6e-6; found by Remez' exchange,
+// its mean error is 1.4e-8), n added to the exponent.
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
+    float a, b;
+    unpair(x, a, b);
+    x = pair(fminf(fmaxf(a, -126.f), 128.f), fminf(fmaxf(b, -126.f), 128.f));
+    const uint64_t t = add2(x, pair(12582912.f, 12582912.f));
+    const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
+    uint64_t r = pair(0.009570102207362652f, 0.009570102207362652f);
+    r = fma2(r, f, pair(0.05591785907745361f, 0.05591785907745361f));
+    r = fma2(r, f, pair(0.240247443318367f, 0.240247443318367f));
+    r = fma2(r, f, pair(0.6931217908859253f, 0.6931217908859253f));
+    r = fma2(r, f, pair(0.9999992847442627f, 0.9999992847442627f));
+    float ta, tb, ra, rb;
+    unpair(t, ta, tb);
+    unpair(r, ra, rb);
+    return pair(__uint_as_float(__float_as_uint(ra) + (__float_as_uint(ta) << 23)),
+                __uint_as_float(__float_as_uint(rb) + (__float_as_uint(tb) << 23)));
+}
+
+// The greatest of 64 scores (NaN if one is).
+__device__ __forceinline__ float half_max(const uint32_t (&u)[2][32]) {
+    float m4[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(u[0][j]);
+#pragma unroll
+    for (int j = 4; j < 64; j += 2)
+        m4[(j >> 1) & 3] = max3_nan(m4[(j >> 1) & 3], __uint_as_float(u[j >> 5][j & 31]),
+                                    __uint_as_float(u[j >> 5][(j + 1) & 31]));
+    return max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+}
+
+// P = 2^(x sl2 + neg_m) of 64 scores, written as bf16 pairs to the 32 TMEM columns at pcol; returns the sum of the
+// unrounded values.  POLY: a quarter of the exponentials on the FMA pipe (not for masked tiles: -inf has to give 0).
+template <bool POLY>
+__device__ __forceinline__ float half_exp(uint32_t pcol, const uint32_t (&u)[2][32], float sl2, float neg_m) {
+    const uint64_t sc = pair(sl2, sl2), nm = pair(neg_m, neg_m);
+    uint64_t sum[4] = {0, 0, 0, 0};
+    uint32_t pk[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        uint64_t x = fma2(pair(__uint_as_float(u[j >> 4][(2 * j) & 31]), __uint_as_float(u[j >> 4][(2 * j + 1) & 31])), sc, nm);
+        float a, b;
+        if (POLY && (j & 3) == 3) {
+            x = exp2_poly(x);
+            unpair(x, a, b);
+        } else {
+            unpair(x, a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            x = pair(a, b);
+        }
+        sum[j & 3] = add2(sum[j & 3], x);
+        pk[j] = pack_bf16x2(a, b);
+    }
+    tc::tmem_st32(pcol, pk);
+    float a, b;
+    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    return a + b;
+}
+
+// Keys of key tile kt: P cached keys in TP tiles, then R new ones.
+__device__ __forceinline__ int tile_keys(int kt, int P, int TP, int R) {
+    return kt < TP ? min(TN, P - kt * TN) : min(TN, R - (kt - TP) * TN);
 }
 
 struct Maps {
@@ -207,12 +328,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
     const uint32_t q_full = bar0 + 8u * (2 * STAGES), q_empty = q_full + 8;
-    auto s_full = [&](int t) { return q_full + 16u + 8u * t; };
-    auto p_full = [&](int t) { return q_full + 32u + 8u * t; };
-    auto pv_done = [&](int t) { return q_full + 48u + 8u * t; };
-    auto o_full = [&](int t) { return q_full + 64u + 8u * t; };
-    auto o_free = [&](int t) { return q_full + 80u + 8u * t; };
-    const uint32_t fin = q_full + 96u;
+    auto s_full = [&](int t, int b) { return q_full + 16u + 8u * (2 * t + b); };
+    auto p_full = [&](int t, int b) { return q_full + 48u + 8u * (2 * t + b); };
+    auto pv_done = [&](int t, int b) { return q_full + 80u + 8u * (2 * t + b); };
+    auto o_full = [&](int t) { return q_full + 112u + 8u * t; };
+    auto o_free = [&](int t) { return q_full + 128u + 8u * t; };
+    auto fin = [&](int i) { return q_full + 144u + 8u * i; };
+    auto seg_full = [&](int i) { return q_full + 176u + 8u * i; };
+    auto seg_empty = [&](int i) { return q_full + 176u + 8u * (SEGS + i); };
+    Segment *segs = reinterpret_cast<Segment *>(smem + L::SEG_OFF);
     Line *line = reinterpret_cast<Line *>(smem + L::LINE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
@@ -223,18 +347,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             tc::mbar_init(full(s), 1);
-            tc::mbar_init(empty(s), 1);
+            tc::mbar_init(empty(s), 2);  // both MMA issuers
         }
         tc::mbar_init(q_full, 1);
-        tc::mbar_init(q_empty, 1);
+        tc::mbar_init(q_empty, 2);
         for (int t = 0; t < 2; ++t) {
-            tc::mbar_init(s_full(t), 1);
-            tc::mbar_init(p_full(t), 128);
-            tc::mbar_init(pv_done(t), 1);
+            for (int b = 0; b < 2; ++b) {
+                tc::mbar_init(s_full(t, b), 1);
+                tc::mbar_init(p_full(t, b), 128);
+                tc::mbar_init(pv_done(t, b), 1);
+            }
             tc::mbar_init(o_full(t), 1);
             tc::mbar_init(o_free(t), 128);
         }
-        tc::mbar_init(fin, 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(fin(i), 1);
+        for (int i = 0; i < SEGS; ++i) {
+            tc::mbar_init(seg_full(i), 1);
+            tc::mbar_init(seg_empty(i), kSegReaders);
+        }
         *abort_flag = 0;
         tc::mbar_fence_init();
         tc::tma_prefetch_desc(&maps.ks);
@@ -271,32 +401,77 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             cum[p.B] = sum;
             line->shared_tiles = ceil_div(S, TN);
-            line->shared = (long long)line->shared_tiles * ((g.shared_rt / 2) * kCostPair + (g.shared_rt & 1) * kCostSingle);
-            line->head = line->shared + (long long)sum * own_unit(g);
-            line->total = line->head * p.Hkv;
+            const int n = gridDim.x;
+            auto lay = [&](int pair, int single) {
+                line->pair = pair;
+                line->single = single;
+                line->shared = (long long)line->shared_tiles * unit(*line, g.shared_rt);
+                line->head = line->shared + (long long)sum * unit(*line, g.own_rt);
+                line->total = line->head * p.Hkv;
+            };
+            lay(kCostPair, kCostSingle);
+            if (line->total < (long long)n * kCostPair) lay(1, 1);
+            line->ncta = (int)min((long long)n, line->total);
         }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const Line ln = *line;
-    if (blockIdx.x == 0) {  // for combine_kernel
-        if (tid == 0) *reinterpret_cast<Line *>(p.ws) = ln;
-        for (int b = tid; b <= p.B; b += THREADS) reinterpret_cast<int *>(p.ws + kLineBytes)[b] = cum[b];
-    }
     const uint32_t tbase = *tmem_slot;
-    const int cta = blockIdx.x, ncta = gridDim.x;
+    const int cta = blockIdx.x;
+    const size_t info = info_bytes((size_t)p.Hkv * g.blocks);
     const long long wl = kWaitCycles;
 
+    // The next segment for the calling thread (`all`: for its whole warp, which calls it together).
+    int seg_at = 0;
+    auto next = [&](Segment &sg, bool all) {
+        const int i = seg_at % SEGS;
+        bool got = tc::mbar_wait(seg_full(i), (seg_at / SEGS) & 1, abort_flag, wl);
+        if (all) got = __all_sync(0xffffffffu, got);
+        if (!got) return false;
+        sg = segs[i];
+        if (all) {
+            int *f = reinterpret_cast<int *>(&sg);
+#pragma unroll
+            for (int e = 0; e < (int)(sizeof(Segment) / 4); ++e) f[e] = __shfl_sync(0xffffffffu, f[e], 0);
+        }
+        if (!all || lane == 0) tc::mbar_arrive(seg_empty(i));
+        ++seg_at;
+        return sg.nt > 0;
+    };
+
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-        Walker walk(ln, g, cum, p.B, cta, ncta);
         Segment sg;
-        if (warp == 0 && lane == 0) {
+        if (warp == 2 && lane == 0) {
+            // ================= scheduler and Q producer =================
+            const uint32_t bytes = (uint32_t)D * p.G * g.RT * 2;
+            Walker walk(*line, g, cum, p.B, cta);
+            bool more = true;
+            int n = 0;
+            for (; more; ++n) {
+                if (n >= SEGS && !tc::mbar_wait(seg_empty(n % SEGS), (n / SEGS - 1) & 1, abort_flag, wl)) break;
+                more = walk.next(sg);
+                segs[n % SEGS] = sg;
+                tc::mbar_arrive(seg_full(n % SEGS));
+                if (!more) break;
+                // for combine_kernel: the CTAs of the block
+                if (sg.i0 == 0) reinterpret_cast<int2 *>(p.ws)[sg.id].x = cta;
+                if (sg.last) reinterpret_cast<int2 *>(p.ws)[sg.id].y = cta;
+                if (n > 0 && !tc::mbar_wait(q_empty, (n - 1) & 1, abort_flag, wl)) break;
+                tc::mbar_arrive_expect_tx(q_full, sg.nt * bytes);
+                for (int t = 0; t < sg.nt; ++t) {
+                    const int z = (sg.b < 0 ? 0 : sg.b * p.R) + sg.row0 + t * g.RT;
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        tc::tma_load_3d(sbase + t * L::Q_TILE + h * TM * 128, &maps.q, h * 64, sg.kvh * p.G, z, q_full);
+                }
+            }
+            if (n > 0) tc::mbar_wait_drain(q_full, (n - 1) & 1, wl);
+        } else if (warp == 0 && lane == 0) {
             // ================= K/V producer =================
             int it = 0;
             bool ok = true;
-            while (ok && walk.next(sg)) {
+            while (ok && next(sg, false)) {
                 const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
                 const int TP = ceil_div(P, TN), np = ceil_div(P, BOXR);
                 const int32_t *pages = sg.b < 0 ? p.shared_table : p.block_table + (size_t)sg.b * p.max_pages;
@@ -341,101 +516,102 @@ __global__ void __launch_bounds__(THREADS, 1)
             // nothing may land after the CTA exits: only the last copy of each stage can still be in flight
             for (int i = max(0, it - STAGES); i < it; ++i)
                 tc::mbar_wait_drain(full(i % STAGES), (i / STAGES) & 1, wl);
-        } else if (warp == 2 && lane == 0) {
-            // ================= Q producer =================
-            const uint32_t bytes = (uint32_t)D * p.G * g.RT * 2;
-            int n = 0;
-            while (walk.next(sg)) {
-                if (n > 0 && !tc::mbar_wait(q_empty, (n - 1) & 1, abort_flag, wl)) break;
-                tc::mbar_arrive_expect_tx(q_full, sg.nt * bytes);
-                for (int t = 0; t < sg.nt; ++t) {
-                    const int z = (sg.b < 0 ? 0 : sg.b * p.R) + (2 * sg.j + t) * g.RT;
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
-                        tc::tma_load_3d(sbase + t * L::Q_TILE + h * TM * 128, &maps.q, h * 64, sg.kvh * p.G, z, q_full);
-                }
-                ++n;
-            }
-            if (n > 0) tc::mbar_wait_drain(q_full, (n - 1) & 1, wl);
-        } else if (warp == 1 && lane == 0) {
-            // ================= MMA issue =================
-            constexpr uint32_t id_qk = tc::idesc_bf16_f32(TM, TN, 0, 0), id_pv = tc::idesc_bf16_f32(TM, D, 0, 1);
-            const uint64_t dq = tc::smem_desc_sw128(sbase, 16, 1024);
+        } else if (warp & 1) {
+            // ================= MMA issue: warp 1 for row tile 0, warp 3 for row tile 1 =================
+            // (The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.)
+            // The tensor core executes the MMAs that one thread issues in their order, so S of half u + 2 is issued right
+            // behind the PV of half u, whose P it overwrites.
+            const int t = __shfl_sync(0xffffffffu, warp >> 1, 0);
+            constexpr uint32_t id_qk = tc::idesc_bf16_f32(TM, TH, 0, 0), id_pv = tc::idesc_bf16_f32(TM, D, 0, 1);
+            const uint64_t dq = tc::smem_desc_sw128(sbase + t * L::Q_TILE, 16, 1024);
             const uint64_t dk = tc::smem_desc_sw128(sKV, 16, 1024);
             const uint64_t dv = tc::smem_desc_sw128(sKV, TN * 128, 1024);
-            constexpr uint64_t kQ = L::Q_TILE >> 4, kS = L::KV_TILE >> 4;
-            int it = 0, n = 0;
-            int np[2] = {0, 0}, npv[2] = {0, 0}, ns[2] = {0, 0};  // P tiles, PVs waited for, segments of each row tile
+            constexpr uint64_t kS = L::KV_TILE >> 4, kHalf = (TH * 128) >> 4;
+            const uint32_t s_col = tbase + t * 128, o_col = tbase + 256 + t * D;
+            int it = 0, n = 0, ns = 0;  // tiles of the ring, segments, segments of this row tile
+            int uq = 0, up = 0;         // halves whose S, whose PV has been issued: half u uses S buffer u & 1
             bool ok = true;
-            // (pv_done(t) is waited for once per PV, in order)
-            auto wait_pv = [&](int t) { return tc::mbar_wait(pv_done(t), npv[t]++ & 1, abort_flag, wl); };
+            const bool one = elect_one();
+            auto commit = [&](uint32_t bar) {
+                if (one) tc::mma_commit(bar);
+            };
+            auto arrive = [&](uint32_t bar) {
+                if (one) tc::mbar_arrive(bar);
+            };
             auto wait_full = [&](int i) { return tc::mbar_wait(full(i % STAGES), (i / STAGES) & 1, abort_flag, wl); };
-            while (ok && walk.next(sg)) {
-                const int nt = sg.nt, nk = sg.i1 - sg.i0;
-                ok = tc::mbar_wait(q_full, n & 1, abort_flag, wl) && wait_full(it);
-                ++n;
-                for (int t = 0; t < nt && ok; ++t) {
-                    if (ns[t] > 0) ok = wait_pv(t);  // the last segment's PV has read its P
+            while (ok && next(sg, true)) {
+                const int nk = sg.i1 - sg.i0;
+                ok = tc::mbar_wait(q_full, n++ & 1, abort_flag, wl);
+                if (!ok) break;
+                if (t >= sg.nt) {  // nothing to multiply here: the other issuer's tiles are freed as they come
+                    arrive(q_empty);
+                    for (int i = 0; i < 2 * nk && ok; ++i, ++it) {
+                        ok = wait_full(it);
+                        if (ok) arrive(empty(it % STAGES));
+                    }
+                    continue;
+                }
+                const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
+                const int TP = ceil_div(P, TN);
+                auto halves = [&](int i) { return tile_keys(sg.i0 + i, P, TP, p.R) > TH ? 2 : 1; };
+                int qi = 0, qh = 0, pi = 0, ph = 0;  // next half of S, of PV: tile of the segment and half of the tile
+                auto issue_s = [&]() {
+                    const int st = (it + 2 * qi) % STAGES, buf = uq & 1;
+                    if (qh == 0 && !wait_full(it + 2 * qi)) return false;
+                    if (one) issue_qk<D>(s_col + buf * TH, dq, dk + st * kS + qh * kHalf, id_qk);
+                    commit(s_full(t, buf));
+                    ++uq;
+                    if (++qh == halves(qi)) {
+                        commit(empty(st));
+                        qh = 0;
+                        if (++qi == nk) commit(q_empty);
+                    }
+                    return true;
+                };
+                ok = issue_s();
+                if (ok && qi < nk) ok = issue_s();
+                for (bool first = true; ok && pi < nk; first = false) {
+                    const int vi = it + 2 * pi + 1, st = vi % STAGES, buf = up & 1;
+                    ok = ph > 0 || wait_full(vi);
+                    if (ok && first && ns > 0) ok = tc::mbar_wait(o_free(t), (ns - 1) & 1, abort_flag, wl);
+                    ok = ok && tc::mbar_wait(p_full(t, buf), (up >> 1) & 1, abort_flag, wl);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    issue_qk<D>(tbase + t * 128, dq + t * kQ, dk + (it % STAGES) * kS, id_qk);
-                    tc::mma_commit(s_full(t));
-                }
-                if (!ok) break;
-                tc::mma_commit(empty(it % STAGES));
-                if (nk == 1) tc::mma_commit(q_empty);
-                for (int i = 0; i < nk && ok; ++i, it += 2) {
-                    const int vst = (it + 1) % STAGES, kst = (it + 2) % STAGES;
-                    const bool more = i + 1 < nk;
-                    for (int t = 0; t < nt && ok; ++t) {
-                        if (t == 0) ok = wait_full(it + 1);
-                        if (ok && i == 0 && ns[t] > 0) ok = tc::mbar_wait(o_free(t), (ns[t] - 1) & 1, abort_flag, wl);
-                        ok = ok && tc::mbar_wait(p_full(t), np[t]++ & 1, abort_flag, wl);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        issue_pv(tbase + 256 + t * D, tbase + t * 128, dv + vst * kS, id_pv, i > 0);
-                        tc::mma_commit(pv_done(t));
-                        if (!more) tc::mma_commit(o_full(t));
-                        if (t == nt - 1) tc::mma_commit(empty(vst));
-                        if (more) {
-                            if (t == 0) ok = wait_full(it + 2);
-                            ok = ok && wait_pv(t);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            issue_qk<D>(tbase + t * 128, dq + t * kQ, dk + kst * kS, id_qk);
-                            tc::mma_commit(s_full(t));
-                            if (t == nt - 1) {
-                                tc::mma_commit(empty(kst));
-                                if (i + 2 == nk) tc::mma_commit(q_empty);
-                            }
-                        }
+                    if (one) issue_pv(o_col, s_col + buf * TH, dv + st * kS + ph * kHalf, id_pv, !first);
+                    commit(pv_done(t, buf));
+                    ++up;
+                    if (++ph == halves(pi)) {
+                        commit(empty(st));
+                        ph = 0;
+                        if (++pi == nk) commit(o_full(t));
                     }
+                    if (qi < nk) ok = issue_s();
                 }
-                for (int t = 0; t < nt; ++t) ++ns[t];
+                it += 2 * nk;
+                ++ns;
             }
-            tc::mma_commit(fin);  // every MMA completes before TMEM is freed
-            tc::mbar_wait_drain(fin, 0, wl);
+            commit(fin(t));  // every MMA completes before TMEM is freed
+            tc::mbar_wait_drain(fin(t), 0, wl);
+            __syncwarp();
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         // ================= softmax: warpgroup t has row tile t =================
         const int t = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
         const int rr = row / p.G;  // row (b, r) within the tile
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const uint32_t s_col = tbase + lane_off + t * 128, o_col = tbase + lane_off + 256 + t * D;
         const float sl2 = p.scale_log2;
-        Walker walk(ln, g, cum, p.B, cta, ncta);
         Segment sg;
         int ring = 0, n_s = 0, n_seg = 0;
         bool ok = true;
-        while (walk.next(sg)) {
+        while (next(sg, true)) {
             const int nk = sg.i1 - sg.i0, ring0 = ring;
             ring += 2 * nk;
             if (t >= sg.nt) continue;
             const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
             const int TP = ceil_div(P, TN);
-            const int r = (2 * sg.j + t) * g.RT + rr;  // row of the sequence, or of the batch (shared)
+            const int r = sg.row0 + t * g.RT + rr;  // row of the sequence, or of the batch (shared)
             const bool valid = rr < g.RT && r < (sg.b < 0 ? p.B * p.R : p.R);
             const bool work = __any_sync(0xffffffffu, valid);
             // visible new keys of row r: [0, vis_lim) and [vis_glo, vis_ghi)
@@ -447,99 +623,98 @@ __global__ void __launch_bounds__(THREADS, 1)
                 vis_ghi = vis_glo + p.k;
             }
             float m_run = -INFINITY, l_run = 0.f;
-            for (int i = 0; i < nk; ++i, ++n_s) {
-                const int kt = sg.i0 + i;
-                bool have = ok && tc::mbar_wait(s_full(t), n_s & 1, abort_flag, wl);
-                ok = __all_sync(0xffffffffu, have);  // TMEM accesses are warp-collective
-                if (!ok) break;
-                const int keys = kt < TP ? min(TN, P - kt * TN) : min(TN, p.R - (kt - TP) * TN);
-                if (work) {
-                    tc::fence_after_sync();
-                    uint32_t u[4][32];
+            for (int i = 0; i < nk && ok; ++i) {
+                const int kt = sg.i0 + i, keys = tile_keys(kt, P, TP, p.R);
+                const int nh = keys > TH ? 2 : 1;
+                for (int h = 0; h < nh; ++h, ++n_s) {
+                    const int buf = n_s & 1;
+                    const uint32_t sc = s_col + buf * TH;
+                    bool have = tc::mbar_wait(s_full(t, buf), (n_s >> 1) & 1, abort_flag, wl);
+                    ok = __all_sync(0xffffffffu, have);  // TMEM accesses are warp-collective
+                    if (!ok) break;
+                    if (work) {
+                        tc::fence_after_sync();
+                        uint32_t u[2][32];
+                        tc::tmem_ld32(sc, u[0]);
+                        tc::tmem_ld32(sc + 32, u[1]);
+                        tc::tmem_wait_ld();
+                        const bool masked = kt >= TP || keys < TH * nh;
+                        if (masked) {  // by select, so that masked scores may be anything
+                            int lo = keys, glo = 0, ghi = 0;
+                            if (kt >= TP) {
+                                const int nn0 = (kt - TP) * TN;
+                                lo = min(vis_lim - nn0, keys);
+                                glo = vis_glo - nn0;
+                                ghi = min(vis_ghi - nn0, keys);
+                            }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, u[c]);
-                    tc::tmem_wait_ld();
-                    if (kt >= TP || keys < TN) {  // by select, so that masked scores may be anything
-                        int lo = keys, glo = 0, ghi = 0;
-                        if (kt >= TP) {
-                            const int nn0 = (kt - TP) * TN;
-                            lo = min(vis_lim - nn0, keys);
-                            glo = vis_glo - nn0;
-                            ghi = min(vis_ghi - nn0, keys);
-                        }
+                            for (int c = 0; c < 2; ++c) {
+                                const int k0 = h * TH + c * 32;
+                                const uint32_t bits = range_bits(0, lo, k0) | range_bits(glo, ghi, k0);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t bits = range_bits(0, lo, c * 32) | range_bits(glo, ghi, c * 32);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) u[c][j] = (bits >> j) & 1u ? u[c][j] : 0xff800000u;
-                        }
-                    }
-                    float m8[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) m8[j] = __uint_as_float(u[0][j]);
-#pragma unroll
-                    for (int j = 8; j < 128; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(u[j >> 5][j & 31]));
-                    const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * sl2;
-                    // the running max is raised only when it grows by more than 2^8: a stale one is exact as long as
-                    // the weights fit, and O is rarely rescaled
-                    const bool grow = mx > m_run + 8.f || (m_run == -INFINITY && mx > -INFINITY);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float f = grow && m_run > -INFINITY ? fast_exp2(m_run - mx) : 1.f;
-                        if (i > 0 && __any_sync(0xffffffffu, f < 1.f)) {
-                            // (S of this tile is complete, so PV of the last one is, and the next awaits this P)
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t v[32];
-                                tc::tmem_ld32(o_col + c * 32, v);
-                                tc::tmem_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                                tc::tmem_st32(o_col + c * 32, v);
+                                for (int j = 0; j < 32; ++j) u[c][j] = (bits >> j) & 1u ? u[c][j] : 0xff800000u;
                             }
                         }
-                        if (grow) {
-                            l_run *= f;
-                            m_run = mx;
+                        // Exponentials against the running max as it stands: a stale one is exact as long as the weights
+                        // fit, whatever their size, so no maximum is taken while their sum stays below 2^16.  Above it
+                        // (a score 2^10 to 2^16 times the running max's weight, or one that is not finite) the max is
+                        // raised and the half done again.  Rows with no visible key so far take their maximum first.
+                        if (__any_sync(0xffffffffu, m_run == -INFINITY)) {
+                            const float mx = half_max(u) * sl2;
+                            if (m_run == -INFINITY && mx > -INFINITY) m_run = mx;
                         }
-                    }
-                    const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-                    float s8[8];
+                        float lt;
+                        while (true) {
+                            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                            lt = masked ? half_exp<false>(sc, u, sl2, neg_m) : half_exp<true>(sc, u, sl2, neg_m);
+                            if (__all_sync(0xffffffffu, lt < 65536.f)) break;
+                            const float mx = half_max(u) * sl2;
+                            const bool grow = mx > m_run && !(lt < 65536.f) && mx < INFINITY;
+                            if (!(mx < INFINITY)) lt = l_run = __int_as_float(0x7fffffff);  // no softmax of such scores
+                            if (!__any_sync(0xffffffffu, grow)) break;
+                            // O is at rest once the last half's PV has completed: the next one awaits this P
+                            if (i + h > 0) {
+                                const bool got = tc::mbar_wait(pv_done(t, buf ^ 1), ((n_s - 1) >> 1) & 1, abort_flag, wl);
+                                ok = __all_sync(0xffffffffu, got);
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                                const float f = grow ? fast_exp2(m_run - mx) : 1.f;
+                                l_run *= f;
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t v[32];
+                                    tc::tmem_ld32(o_col + c * 32, v);
+                                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s8[j] = 0.f;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float a = fast_exp2(fmaf(__uint_as_float(u[2 * h + (j >> 4)][(2 * j) & 31]), sl2, neg_m));
-                            const float e =
-                                fast_exp2(fmaf(__uint_as_float(u[2 * h + (j >> 4)][(2 * j + 1) & 31]), sl2, neg_m));
-                            s8[(2 * j) & 7] += a;
-                            s8[(2 * j + 1) & 7] += e;
-                            pk[j] = pack_bf16x2(a, e);
+                                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                                    tc::tmem_st32(o_col + c * 32, v);
+                                }
+                            }
+                            if (grow) m_run = mx;
+                            tc::tmem_wait_st();  // the redone P overwrites the first pass's
                         }
-                        tc::tmem_st32(s_col + h * 32, pk);
+                        if (!ok) break;
+                        l_run += lt;
                     }
-                    l_run += ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
-                }
-                if (t == 0 && keys < TN) {
-                    // keys past the end: zero their V rows (0 * garbage could be NaN) before any PV reads them
-                    const int vi = ring0 + 2 * i + 1, st = vi % STAGES;
-                    const bool got = tc::mbar_wait(full(st), (vi / STAGES) & 1, abort_flag, wl);
-                    ok = __all_sync(0xffffffffu, got);
-                    if (!ok) break;
-                    uint8_t *vrow = smem + L::KV_OFF + st * L::KV_TILE;
-                    for (int idx = row; idx < (TN - keys) * (D / 8); idx += 128) {
-                        const int j = keys + idx / (D / 8), c = idx % (D / 8);
-                        *reinterpret_cast<uint4 *>(vrow + (c >> 3) * TN * 128 + j * 128 + ((c & 7) << 4)) =
-                            make_uint4(0, 0, 0, 0);
+                    if (h == nh - 1 && keys < TH * nh) {
+                        // keys past the end: zero their V rows (0 * garbage could be NaN) before this row tile's PV
+                        // reads them (with two row tiles both do)
+                        const int vi = ring0 + 2 * i + 1, st = vi % STAGES;
+                        const bool got = tc::mbar_wait(full(st), (vi / STAGES) & 1, abort_flag, wl);
+                        ok = __all_sync(0xffffffffu, got);
+                        if (!ok) break;
+                        uint8_t *vrow = smem + L::KV_OFF + st * L::KV_TILE;
+                        for (int idx = row; idx < (TH * nh - keys) * (D / 8); idx += 128) {
+                            const int j = keys + idx / (D / 8), c = idx % (D / 8);
+                            *reinterpret_cast<uint4 *>(vrow + (c >> 3) * TN * 128 + j * 128 + ((c & 7) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_proxy_async_smem();
                     }
-                    tc::fence_proxy_async_smem();
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(p_full(t, buf));
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                tc::mbar_arrive(p_full(t));
             }
             tc::tmem_wait_st();
             // ---- the record: the row over its largest magnitude as fp16 (|error| <= 2^-12 of it) and an fp32 scale ----
@@ -559,7 +734,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float amax = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
                 const float rs = amax > 0.f ? __fdividef(1.f, amax) : 0.f;
                 if (valid) {
-                    uint8_t *rec = p.ws + info_bytes(p.B) + ((size_t)sg.slot * 2 + t) * tile_record_bytes(D);
+                    uint8_t *rec = p.ws + info + ((size_t)(cta + sg.id) * 2 + t) * tile_record_bytes(D);
                     uint4 *vals = reinterpret_cast<uint4 *>(rec) + row;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
@@ -591,7 +766,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Joins the records of 32 rows (lane = row) of one KV head; warp w has columns [8w, 8w + 8).  Also reports lengths and
 // pages out of range and leaves those rows alone.
 template <int D>
-__global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p, int ncta) {
+__global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p) {
     __shared__ int bad_seq[32];
     const int lane = threadIdx.x & 31, chunk = threadIdx.x >> 5;
     const int kvh = blockIdx.y;
@@ -628,29 +803,26 @@ __global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p
         if (chunk == 0) atomicOr(p.dev_status, bits);
         return;
     }
-    const Line ln = *reinterpret_cast<const Line *>(p.ws);
-    const int *cum = reinterpret_cast<const int *>(p.ws + kLineBytes);
-    const uint8_t *recs = p.ws + info_bytes(p.B);
     // the two blocks that hold this row: shared (x = 0) and own (x = 1)
     const int sr = b * p.R + r, st = sr / g.RT, ot = r / g.RT;
-    Block bl[2] = {shared_block(ln, g, kvh, st / 2), own_block(ln, g, kvh, cum[b], cum[b + 1], ot / 2)};
     const int id[2] = {kvh * g.blocks + st / 2, kvh * g.blocks + g.shared_blocks + b * g.own_blocks + ot / 2};
-    const int tile[2] = {st & 1, ot & 1};
     const int row[2] = {(sr - st * g.RT) * p.G + gq, (r - ot * g.RT) * p.G + gq};
+    const size_t rec_bytes = tile_record_bytes(D);
+    const uint8_t *recs = p.ws + info_bytes((size_t)p.Hkv * g.blocks);
+    const uint8_t *rec[2];
+    int count[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int2 c = x == 0 && S == 0 ? make_int2(0, -1) : reinterpret_cast<const int2 *>(p.ws)[id[x]];
+        count[x] = c.y - c.x + 1;
+        rec[x] = recs + ((size_t)(c.x + id[x]) * 2 + ((x == 0 ? st : ot) & 1)) * rec_bytes;
+    }
     float mx = -INFINITY;
     // every record of the row, in the order of the line
     auto each = [&](auto &&f) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            if (bl[x].tiles == 0) continue;
-            const int c0 = (int)(bl[x].start * ncta / ln.total);
-            const int c1 = (int)((bl[x].start + (long long)(bl[x].tiles - 1) * bl[x].w) * ncta / ln.total);
-            for (int c = c0; c <= c1; ++c) {
-                int i0, i1;
-                tiles_in(bl[x], cut(ln.total, c, ncta), cut(ln.total, c + 1, ncta), i0, i1);
-                if (i0 < i1) f(recs + ((size_t)(c + id[x]) * 2 + tile[x]) * tile_record_bytes(D), row[x]);
-            }
-        }
+        for (int x = 0; x < 2; ++x)
+            for (int c = 0; c < count[x]; ++c) f(rec[x] + c * 2 * rec_bytes, row[x]);
     };
     each([&](const uint8_t *rec, int rw) {
         mx = fmaxf(mx, reinterpret_cast<const float2 *>(rec + TM * D * 2)[rw].x);
@@ -752,7 +924,7 @@ cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(((long long)p.B * p.R * p.G + 31) / 32), p.Hkv, 1);
     cfg.blockDim = dim3(D * 4, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, p, kNumSMs);
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -762,7 +934,7 @@ cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
 size_t shared_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int R, int, int) {
     const Geometry g = geometry(B, R, Hq / Hkv);
     // a segment's record is at cta + block: along the line both only grow, and one of them from segment to segment
-    return info_bytes(B) + ((size_t)kNumSMs + (size_t)Hkv * g.blocks) * 2 * tile_record_bytes(D);
+    return info_bytes((size_t)Hkv * g.blocks) + ((size_t)kNumSMs + (size_t)Hkv * g.blocks) * 2 * tile_record_bytes(D);
 }
 
 cudaError_t shared_attn_launch(const SharedAttnParams &p, cudaStream_t s) {
