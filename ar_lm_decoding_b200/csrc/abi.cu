@@ -295,6 +295,7 @@ tidar_status check_shared(int B, int Hq, int Hkv, int D, int R, int S_max, int P
     if (Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128) || B > kMaxBatchShared || R > kMaxCausalRows)
         return TIDAR_ERR_UNSUPPORTED;
     if ((long long)B * R * Hq >= (1LL << 31)) return TIDAR_ERR_UNSUPPORTED;
+    if (!shared_attn_fits(B, R, Hkv, Hq / Hkv, S_max, P_max)) return TIDAR_ERR_UNSUPPORTED;
     return TIDAR_OK;
 }
 

@@ -27,6 +27,8 @@ struct SharedAttnParams {
     int32_t *dev_status;
 };
 
+// Whether the cost of the call's key tiles counts in 32 bits.
+bool shared_attn_fits(int B, int R, int Hkv, int G, int S_max, int P_max);
 size_t shared_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max);
 cudaError_t shared_attn_launch(const SharedAttnParams &p, cudaStream_t s);
 

@@ -23,10 +23,8 @@
 // the round trip P -> PV -> next S is off its path.  (Whole tiles of 128 keys in one buffer each, as TMEM holds no more
 // at D = 128, left the softmax waiting 2,240 of 4,395 cycles per tile on that round trip.)
 //
-// The exponentials bound the softmax (a warp-wide ex2 takes ~9 cycles of its sub-partition's MUFU): a quarter of them
-// is taken by a polynomial on the FMA pipe, and scaling and sums use the packed fp32 pair instructions.  128 values per
-// thread, two warps per sub-partition, measured alone: 2,497 cycles, packed 2,269, with the quarter 1,903, with a half
-// 1,999.
+// Scaling and sums use the packed fp32 pair instructions (64 values per thread, two warps per sub-partition, measured
+// alone: 1,224 cycles scalar, 1,126 packed, of which the MUFU's ex2 are about 1,000).
 #include "cache_ops.cuh"
 #include "tc.cuh"
 
@@ -39,20 +37,21 @@ constexpr int TN = 128;
 constexpr int TH = 64;  // keys of half a tile
 constexpr int THREADS = 384;
 constexpr int BOXR = kPageRows;
-// Cost of one key tile for a block of two row tiles and of one (where every CTA has a few tiles; see Line).
-constexpr int kCostPair = 3, kCostSingle = 2;
+// Cost of one key tile for a block of two row tiles and of one, and of a block's start and end (Q, the record), where
+// every CTA has a few tiles (see Line): measured ~3,900, ~2,700 and ~3,000 cycles.
+constexpr int kCostPair = 3, kCostSingle = 2, kCostBlock = 2;
 constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
 
-// The line of key tiles (cum[b], beside it: key tiles of the sequences before b).  Every CTA's share is at least the
-// cost of one tile, so the CTAs from a block's first tile to its last all have a part of it: where there are fewer
-// tiles than CTAs every tile costs 1 and that many CTAs work.
+// The line of key tiles (cum[b], beside it: key tiles of the sequences before b, nseq[b]: sequences before b that have
+// any).  Every CTA's share is at least the cost of one tile, so the CTAs from a block's first tile to its last all have
+// a part of it: where there are too few tiles for that every tile costs 1 and as many CTAs work as there are tiles.
 struct Line {
-    long long total;   // cost of all KV heads
-    long long head;    // cost of one KV head
-    long long shared;  // of its shared blocks
-    int shared_tiles;  // key tiles of the shared prefix
-    int pair, single;  // cost of a key tile for two row tiles, for one
-    int ncta;          // CTAs that work
+    int total;               // cost of all KV heads
+    int head;                // cost of one KV head
+    int shared;              // of its shared blocks
+    int shared_tiles;        // key tiles of the shared prefix
+    int pair, single, block; // cost of a key tile for two row tiles, for one, and of a block beside its tiles
+    int ncta;                // CTAs that work
 };
 
 __host__ __device__ __forceinline__ int rows_per_tile(int G) { return TM / G; }
@@ -77,30 +76,23 @@ __host__ __device__ __forceinline__ Geometry geometry(int B, int R, int G) {
 }
 
 // First position of CTA c of n on a line of length total: the position s belongs to CTA floor(s n / total).
-__device__ __forceinline__ long long cut(long long total, int c, int n) { return (total * c + n - 1) / n; }
-
-// A block of the line: `tiles` key tiles of cost `w` each from position `start`.
-struct Block {
-    long long start;
-    int tiles, w;
-};
-__device__ __forceinline__ Block shared_block(const Line &ln, const Geometry &g, int kvh, int j) {
-    const bool pair = 2 * j + 1 < g.shared_rt;
-    return Block{kvh * ln.head + (long long)j * ln.shared_tiles * ln.pair, ln.shared_tiles, pair ? ln.pair : ln.single};
+__device__ __forceinline__ int cut(int total, int c, int n) {
+    const int q = total / n, r = total - q * n;
+    return q * c + (r * c + n - 1) / n;
 }
-// cost of one key tile over n row tiles
-__device__ __forceinline__ int unit(const Line &ln, int n) { return (n / 2) * ln.pair + (n & 1) * ln.single; }
-__device__ __forceinline__ Block own_block(const Line &ln, const Geometry &g, int kvh, int cum0, int cum1, int j) {
-    const bool pair = 2 * j + 1 < g.own_rt;
-    const int tiles = cum1 - cum0;
-    return Block{kvh * ln.head + ln.shared + (long long)cum0 * unit(ln, g.own_rt) + (long long)j * tiles * ln.pair, tiles,
-                 pair ? ln.pair : ln.single};
+
+// A block of the line: `tiles` key tiles of cost `w` each from position `start`, the first of cost block + w.
+struct Block {
+    int start, tiles, w;
+};
+// Cost of n row tiles' blocks against `tiles` key tiles.
+__device__ __forceinline__ int blocks_cost(const Line &ln, int n, int tiles) {
+    return (n / 2) * (ln.block + tiles * ln.pair) + (n & 1) * (ln.block + tiles * ln.single);
 }
 // Tiles [i0, i1) of a block whose positions fall in [x0, x1).
-__device__ __forceinline__ void tiles_in(const Block &bl, long long x0, long long x1, int &i0, int &i1) {
-    const long long a = x0 - bl.start, b = x1 - bl.start;
-    i0 = a <= 0 ? 0 : (int)min((a + bl.w - 1) / bl.w, (long long)bl.tiles);
-    i1 = b <= 0 ? 0 : (int)min((b + bl.w - 1) / bl.w, (long long)bl.tiles);
+__device__ __forceinline__ int first_tile(const Line &ln, const Block &bl, int x) {
+    const int a = x - bl.start;
+    return a <= 0 ? 0 : min(max(1, (a - ln.block + bl.w - 1) / bl.w), bl.tiles);
 }
 
 // One run of key tiles of one block, as a CTA works on it.
@@ -110,56 +102,61 @@ struct __align__(16) Segment {
     int row0;        // first row (of the sequence, or of the batch) of the block's first row tile
     int nt;          // row tiles (1 or 2; 0: no more segments)
     int id;          // block
-    int last;        // the run ends the block
+    int len;         // cached keys (the shared or the sequence's own length)
 };
 
 // Walks the segments of a CTA's share [x0, x1).
 struct Walker {
     const Line &ln;
     const Geometry &g;
-    const int *cum;
-    int B, cta;
-    long long pos, x1, x0;
-    __device__ Walker(const Line &l, const Geometry &ge, const int *c, int B_, int cta_)
-        : ln(l), g(ge), cum(c), B(B_), cta(cta_) {
+    const int *cum, *nseq;
+    int B, cta, x0, x1, pos;
+    bool last;  // the segment ends its block
+    __device__ Walker(const Line &l, const Geometry &ge, const int *c, const int *ns, int B_, int cta_)
+        : ln(l), g(ge), cum(c), nseq(ns), B(B_), cta(cta_) {
         x0 = pos = cta < l.ncta ? cut(l.total, cta_, l.ncta) : 0;
         x1 = cta < l.ncta ? cut(l.total, cta_ + 1, l.ncta) : 0;
     }
+    // cost of the own blocks of the sequences before b
+    __device__ int own_before(int b) const {
+        return cum[b] * ((g.own_rt / 2) * ln.pair + (g.own_rt & 1) * ln.single) + nseq[b] * g.own_blocks * ln.block;
+    }
     __device__ bool next(Segment &s) {
         while (pos < x1) {
-            const int kvh = (int)(pos / ln.head);
-            const long long rem = pos - kvh * ln.head;
+            const int kvh = pos / ln.head, rem = pos - kvh * ln.head;
             Block bl;
-            int id;
+            int rt, j;
             s.kvh = kvh;
             if (rem < ln.shared) {
+                rt = g.shared_rt;
+                bl.tiles = ln.shared_tiles;
+                const int per = ln.block + bl.tiles * ln.pair;
+                j = rem / per;
+                bl.start = kvh * ln.head + j * per;
                 s.b = -1;
-                const int j = (int)(rem / ((long long)ln.shared_tiles * ln.pair));
-                bl = shared_block(ln, g, kvh, j);
-                s.nt = 2 * j + 1 < g.shared_rt ? 2 : 1;
-                s.row0 = 2 * j * g.RT;
-                id = j;
+                s.id = kvh * g.blocks + j;
             } else {
-                const long long r2 = rem - ln.shared;
-                const int ou = unit(ln, g.own_rt), at = (int)(r2 / ou);
-                int lo = 0, hi = B;  // the b with cum[b] <= at < cum[b + 1]
+                int lo = 0, hi = B;  // the sequence whose blocks hold the position
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (cum[mid] <= at) lo = mid;
+                    if (own_before(mid) <= rem - ln.shared) lo = mid;
                     else hi = mid;
                 }
+                rt = g.own_rt;
+                bl.tiles = cum[lo + 1] - cum[lo];
+                const int per = ln.block + bl.tiles * ln.pair, at = own_before(lo);
+                j = (rem - ln.shared - at) / per;
+                bl.start = kvh * ln.head + ln.shared + at + j * per;
                 s.b = lo;
-                const int tiles = cum[lo + 1] - cum[lo];
-                const int j = (int)((r2 - (long long)cum[lo] * ou) / ((long long)tiles * ln.pair));
-                bl = own_block(ln, g, kvh, cum[lo], cum[lo + 1], j);
-                s.nt = 2 * j + 1 < g.own_rt ? 2 : 1;
-                s.row0 = 2 * j * g.RT;
-                id = g.shared_blocks + lo * g.own_blocks + j;
+                s.id = kvh * g.blocks + g.shared_blocks + lo * g.own_blocks + j;
             }
-            tiles_in(bl, x0, x1, s.i0, s.i1);
-            s.id = kvh * g.blocks + id;
-            s.last = s.i1 == bl.tiles;
-            pos = bl.start + (long long)bl.tiles * bl.w;
+            s.nt = 2 * j + 1 < rt ? 2 : 1;
+            s.row0 = 2 * j * g.RT;
+            bl.w = s.nt == 2 ? ln.pair : ln.single;
+            s.i0 = first_tile(ln, bl, x0);
+            s.i1 = first_tile(ln, bl, x1);
+            last = s.i1 == bl.tiles;
+            pos = bl.start + ln.block + bl.tiles * bl.w;
             if (s.i0 < s.i1) return true;
         }
         s.nt = 0;
@@ -182,12 +179,12 @@ struct Smem {
     static constexpr int SEG_OFF = (BAR_OFF + NBARS * 8 + 63) / 64 * 64;
     static constexpr int LINE_OFF = SEG_OFF + SEGS * (int)sizeof(Segment);
     static constexpr int MISC_OFF = LINE_OFF + 64;
-    static constexpr int CUM_OFF = MISC_OFF + 16;  // int[B + 1]
-    static int alloc(int B) { return CUM_OFF + (B + 1) * 4 + 1024; }
+    static constexpr int CUM_OFF = MISC_OFF + 16;  // int[B + 1] twice
+    static int alloc(int B) { return CUM_OFF + 2 * (B + 1) * 4 + 1024; }
 };
 static_assert(sizeof(Line) <= 64, "the line's place in shared memory");
-static_assert(Smem<128>::CUM_OFF + (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024 &&
-                  Smem<64>::CUM_OFF + (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024,
+static_assert(Smem<128>::CUM_OFF + 2 * (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024 &&
+                  Smem<64>::CUM_OFF + 2 * (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024,
               "shared memory beyond 227 KB");
 
 // One lane of the (converged) warp, the same one every time.
@@ -246,27 +243,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
-// 2^x of both halves on the FMA pipe (below -126: 2^-126; from 128, and NaN: infinite or out of range): x = n + f, n the nearest integer (by adding and
-// taking away 1.5 2^23), 2^f by the quartic of least relative error on [-1/2, 1/2] (2.6e-6; found by Remez' exchange,
-// its mean error is 1.4e-8), n added to the exponent.
-__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
-    float a, b;
-    unpair(x, a, b);
-    x = pair(fminf(fmaxf(a, -126.f), 128.f), fminf(fmaxf(b, -126.f), 128.f));
-    const uint64_t t = add2(x, pair(12582912.f, 12582912.f));
-    const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
-    uint64_t r = pair(0.009570102207362652f, 0.009570102207362652f);
-    r = fma2(r, f, pair(0.05591785907745361f, 0.05591785907745361f));
-    r = fma2(r, f, pair(0.240247443318367f, 0.240247443318367f));
-    r = fma2(r, f, pair(0.6931217908859253f, 0.6931217908859253f));
-    r = fma2(r, f, pair(0.9999992847442627f, 0.9999992847442627f));
-    float ta, tb, ra, rb;
-    unpair(t, ta, tb);
-    unpair(r, ra, rb);
-    return pair(__uint_as_float(__float_as_uint(ra) + (__float_as_uint(ta) << 23)),
-                __uint_as_float(__float_as_uint(rb) + (__float_as_uint(tb) << 23)));
-}
-
 // The greatest of 64 scores (NaN if one is).
 __device__ __forceinline__ float half_max(const uint32_t (&u)[2][32]) {
     float m4[4];
@@ -279,33 +255,79 @@ __device__ __forceinline__ float half_max(const uint32_t (&u)[2][32]) {
     return max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
 }
 
-// P = 2^(x sl2 + neg_m) of 64 scores, written as bf16 pairs to the 32 TMEM columns at pcol; returns the sum of the
-// unrounded values.  POLY: a quarter of the exponentials on the FMA pipe (not for masked tiles: -inf has to give 0).
-template <bool POLY>
-__device__ __forceinline__ float half_exp(uint32_t pcol, const uint32_t (&u)[2][32], float sl2, float neg_m) {
+// 64 scores of this thread's row; those of the keys k0 + j outside [0, lo) and [glo, ghi) become -inf (by select, so that
+// they may hold anything).
+__device__ __forceinline__ void load_scores(uint32_t sc, uint32_t (&u)[2][32]) {
+    tc::fence_after_sync();
+    tc::tmem_ld32(sc, u[0]);
+    tc::tmem_ld32(sc + 32, u[1]);
+    tc::tmem_wait_ld();
+}
+__device__ __forceinline__ void mask_scores(uint32_t (&u)[2][32], int k0, int lo, int glo, int ghi) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t bits = range_bits(0, lo, k0 + c * 32) | range_bits(glo, ghi, k0 + c * 32);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u[c][j] = (bits >> j) & 1u ? u[c][j] : 0xff800000u;
+    }
+}
+
+// P = 2^(x sl2 + neg_m) of 64 scores as bf16 pairs; returns the sum of the unrounded values.
+__device__ __forceinline__ float half_exp(const uint32_t (&u)[2][32], float sl2, float neg_m, uint32_t (&pk)[32]) {
     const uint64_t sc = pair(sl2, sl2), nm = pair(neg_m, neg_m);
     uint64_t sum[4] = {0, 0, 0, 0};
-    uint32_t pk[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        uint64_t x = fma2(pair(__uint_as_float(u[j >> 4][(2 * j) & 31]), __uint_as_float(u[j >> 4][(2 * j + 1) & 31])), sc, nm);
+        const uint64_t x =
+            fma2(pair(__uint_as_float(u[j >> 4][(2 * j) & 31]), __uint_as_float(u[j >> 4][(2 * j + 1) & 31])), sc, nm);
         float a, b;
-        if (POLY && (j & 3) == 3) {
-            x = exp2_poly(x);
-            unpair(x, a, b);
-        } else {
-            unpair(x, a, b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            x = pair(a, b);
-        }
-        sum[j & 3] = add2(sum[j & 3], x);
+        unpair(x, a, b);
+        a = fast_exp2(a);
+        b = fast_exp2(b);
+        sum[j & 3] = add2(sum[j & 3], pair(a, b));
         pk[j] = pack_bf16x2(a, b);
     }
-    tc::tmem_st32(pcol, pk);
     float a, b;
     unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
     return a + b;
+}
+
+// The running max m of a row is raised to the maximum of the half at sc, where the row has none yet or its weights
+// against m sum to lt >= 2^16 (or are not finite), and O and the row's sum l are scaled to it.  (A call of its own: it is
+// rare, and inlined it would spread the loop over the instruction cache.)
+struct RowState {
+    float m, l;
+    int ok;
+};
+template <int D>
+__device__ __noinline__ RowState raise_max(uint32_t sc, int k0, int lo, int glo, int ghi, float sl2, float lt, float m, float l,
+                                           uint32_t o_col, uint32_t pv_bar, uint32_t pv_phase, volatile int *abort_flag) {
+    uint32_t u[2][32];
+    load_scores(sc, u);
+    mask_scores(u, k0, lo, glo, ghi);
+    const float mx = half_max(u) * sl2;
+    RowState st{m, l, 1};
+    if (!(mx < INFINITY)) st.l = __int_as_float(0x7fffffff);  // a score of NaN or infinity: no softmax
+    const bool grow = mx > m && mx < INFINITY && (m == -INFINITY || !(lt < 65536.f));
+    const float f = grow && m > -INFINITY ? fast_exp2(m - mx) : 1.f;
+    if (__any_sync(0xffffffffu, f < 1.f)) {
+        // O is at rest once the last half's PV has completed: the next one awaits this half's P
+        st.ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_bar, pv_phase, abort_flag, kWaitCycles));
+        if (!st.ok) return st;
+        tc::fence_after_sync();
+        st.l *= f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tc::tmem_ld32(o_col + c * 32, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+            tc::tmem_st32(o_col + c * 32, v);
+        }
+    }
+    if (grow) st.m = mx;
+    return st;
 }
 
 // Keys of key tile kt: P cached keys in TP tiles, then R new ones.
@@ -340,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     Line *line = reinterpret_cast<Line *>(smem + L::LINE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
-    int *cum = reinterpret_cast<int *>(smem + L::CUM_OFF);
+    int *cum = reinterpret_cast<int *>(smem + L::CUM_OFF), *nseq = cum + p.B + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Geometry g = geometry(p.B, p.R, p.G);
 
@@ -381,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int S = p.shared_len[0];
     if (S < 0 || S > p.S_max) S = 0;  // (combine_kernel reports it and writes nothing)
     if (warp == 3) {  // the line: key tiles of every sequence (none where the length is out of range)
-        int sum = 0;
+        int sum = 0, seqs = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             int x = 0;
@@ -395,23 +417,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int y = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += y;
             }
-            if (b < p.B) cum[b] = sum + inc - x;
+            const uint32_t any = __ballot_sync(0xffffffffu, x > 0);
+            if (b < p.B) {
+                cum[b] = sum + inc - x;
+                nseq[b] = seqs + __popc(any & ((1u << lane) - 1u));
+            }
             sum += __shfl_sync(0xffffffffu, inc, 31);
+            seqs += __popc(any);
         }
         if (lane == 0) {
             cum[p.B] = sum;
-            line->shared_tiles = ceil_div(S, TN);
-            const int n = gridDim.x;
-            auto lay = [&](int pair, int single) {
-                line->pair = pair;
-                line->single = single;
-                line->shared = (long long)line->shared_tiles * unit(*line, g.shared_rt);
-                line->head = line->shared + (long long)sum * unit(*line, g.own_rt);
-                line->total = line->head * p.Hkv;
+            nseq[p.B] = seqs;
+            const int st = ceil_div(S, TN), n = gridDim.x;
+            Line l;
+            l.shared_tiles = st;
+            auto lay = [&](int pair, int single, int block) {
+                l.pair = pair;
+                l.single = single;
+                l.block = block;
+                l.shared = st > 0 ? blocks_cost(l, g.shared_rt, st) : 0;
+                l.head = l.shared + (g.own_rt / 2) * (seqs * block + sum * pair) + (g.own_rt & 1) * (seqs * block + sum * single);
+                l.total = l.head * p.Hkv;
             };
-            lay(kCostPair, kCostSingle);
-            if (line->total < (long long)n * kCostPair) lay(1, 1);
-            line->ncta = (int)min((long long)n, line->total);
+            lay(kCostPair, kCostSingle, kCostBlock);
+            if (l.total < n * (kCostPair + kCostBlock)) lay(1, 1, 0);
+            l.ncta = min(n, l.total);
+            *line = l;
         }
     }
     tc::fence_before_sync();
@@ -445,18 +476,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 2 && lane == 0) {
             // ================= scheduler and Q producer =================
             const uint32_t bytes = (uint32_t)D * p.G * g.RT * 2;
-            Walker walk(*line, g, cum, p.B, cta);
+            Walker walk(*line, g, cum, nseq, p.B, cta);
             bool more = true;
             int n = 0;
             for (; more; ++n) {
                 if (n >= SEGS && !tc::mbar_wait(seg_empty(n % SEGS), (n / SEGS - 1) & 1, abort_flag, wl)) break;
                 more = walk.next(sg);
+                sg.len = !more ? 0 : sg.b < 0 ? S : p.prefix_len[sg.b];
                 segs[n % SEGS] = sg;
                 tc::mbar_arrive(seg_full(n % SEGS));
                 if (!more) break;
                 // for combine_kernel: the CTAs of the block
                 if (sg.i0 == 0) reinterpret_cast<int2 *>(p.ws)[sg.id].x = cta;
-                if (sg.last) reinterpret_cast<int2 *>(p.ws)[sg.id].y = cta;
+                if (walk.last) reinterpret_cast<int2 *>(p.ws)[sg.id].y = cta;
                 if (n > 0 && !tc::mbar_wait(q_empty, (n - 1) & 1, abort_flag, wl)) break;
                 tc::mbar_arrive_expect_tx(q_full, sg.nt * bytes);
                 for (int t = 0; t < sg.nt; ++t) {
@@ -472,8 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int it = 0;
             bool ok = true;
             while (ok && next(sg, false)) {
-                const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
-                const int TP = ceil_div(P, TN), np = ceil_div(P, BOXR);
+                const int P = sg.len, TP = ceil_div(P, TN), np = ceil_div(P, BOXR);
                 const int32_t *pages = sg.b < 0 ? p.shared_table : p.block_table + (size_t)sg.b * p.max_pages;
                 for (int i = sg.i0; i < sg.i1 && ok; ++i) {
 #pragma unroll 1
@@ -519,8 +550,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp & 1) {
             // ================= MMA issue: warp 1 for row tile 0, warp 3 for row tile 1 =================
             // (The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.)
-            // The tensor core executes the MMAs that one thread issues in their order, so S of half u + 2 is issued right
-            // behind the PV of half u, whose P it overwrites.
+            // The tensor core executes the MMAs that one thread issues in their order, so S of half tile u + 2 is issued
+            // right behind the PV of half tile u, whose P it overwrites.  S runs ahead of PV across segments too, so that
+            // the next segment's first scores are there when the softmax has written the last record.
             const int t = __shfl_sync(0xffffffffu, warp >> 1, 0);
             constexpr uint32_t id_qk = tc::idesc_bf16_f32(TM, TH, 0, 0), id_pv = tc::idesc_bf16_f32(TM, D, 0, 1);
             const uint64_t dq = tc::smem_desc_sw128(sbase + t * L::Q_TILE, 16, 1024);
@@ -528,9 +560,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint64_t dv = tc::smem_desc_sw128(sKV, TN * 128, 1024);
             constexpr uint64_t kS = L::KV_TILE >> 4, kHalf = (TH * 128) >> 4;
             const uint32_t s_col = tbase + t * 128, o_col = tbase + 256 + t * D;
-            int it = 0, n = 0, ns = 0;  // tiles of the ring, segments, segments of this row tile
-            int uq = 0, up = 0;         // halves whose S, whose PV has been issued: half u uses S buffer u & 1
-            bool ok = true;
             const bool one = elect_one();
             auto commit = [&](uint32_t bar) {
                 if (one) tc::mma_commit(bar);
@@ -538,60 +567,121 @@ __global__ void __launch_bounds__(THREADS, 1)
             auto arrive = [&](uint32_t bar) {
                 if (one) tc::mbar_arrive(bar);
             };
-            auto wait_full = [&](int i) { return tc::mbar_wait(full(i % STAGES), (i / STAGES) & 1, abort_flag, wl); };
-            while (ok && next(sg, true)) {
-                const int nk = sg.i1 - sg.i0;
-                ok = tc::mbar_wait(q_full, n++ & 1, abort_flag, wl);
-                if (!ok) break;
-                if (t >= sg.nt) {  // nothing to multiply here: the other issuer's tiles are freed as they come
-                    arrive(q_empty);
-                    for (int i = 0; i < 2 * nk && ok; ++i, ++it) {
-                        ok = wait_full(it);
-                        if (ok) arrive(empty(it % STAGES));
+            auto wait = [&](uint32_t bar, uint32_t ph) {
+                return __all_sync(0xffffffffu, tc::mbar_wait(bar, ph, abort_flag, wl)) != 0;
+            };
+            auto wait_full = [&](int i) { return wait(full(i % STAGES), (i / STAGES) & 1); };
+            // A place on the segments: half h of key tile i of [first, last), whose K is tile `ring` of the ring.
+            struct Cursor {
+                int seg;         // segments taken
+                int i, h, first, last, ring;
+                int one0, one1;  // key tiles of 64 keys or fewer: the cached tail, the new keys' tail (-1: none)
+                bool in;         // inside a segment
+            };
+            Cursor q{0, 0, 0, 0, 0, 0, -1, -1, false}, v{0, 0, 0, 0, 0, 0, -1, -1, false};
+            int ns = 0;                  // segments of the PV
+            uint32_t pph = 0, busy = 0;  // phases of p_full; S buffers (h of the half) whose PV is not issued yet
+            bool ok = true, more = true;
+            auto read = [&](Cursor &c, Segment &sg) {  // segment c.seg
+                if (!wait(seg_full(c.seg % SEGS), (c.seg / SEGS) & 1)) return false;
+                sg = segs[c.seg % SEGS];
+                int *f = reinterpret_cast<int *>(&sg);
+#pragma unroll
+                for (int e = 0; e < (int)(sizeof(Segment) / 4); ++e) f[e] = __shfl_sync(0xffffffffu, f[e], 0);
+                return true;
+            };
+            auto enter = [&](Cursor &c, const Segment &sg) {
+                const int P = sg.len, TP = ceil_div(P, TN);
+                c.i = c.first = sg.i0;
+                c.last = sg.i1;
+                c.h = 0;
+                const int new_last = TP + ceil_div(p.R, TN) - 1;
+                c.one0 = TP > 0 && tile_keys(TP - 1, P, TP, p.R) <= TH ? TP - 1 : -1;
+                c.one1 = tile_keys(new_last, P, TP, p.R) <= TH ? new_last : -1;
+                c.in = true;
+                ++c.seg;
+            };
+            auto halves = [&](const Cursor &c) { return c.i == c.one0 || c.i == c.one1 ? 1 : 2; };
+            while (ok) {
+                while (busy != 3 && more) {  // S
+                    if (!q.in) {
+                        Segment sg;
+                        ok = read(q, sg);
+                        if (!ok) break;
+                        if (sg.nt == 0) {
+                            more = false;
+                            break;
+                        }
+                        if (t >= sg.nt) {  // nothing to multiply here: the tiles are freed as they come, once no PV is due
+                            if (busy) break;
+                            ok = wait(q_full, q.seg & 1);
+                            if (!ok) break;
+                            arrive(q_empty);
+                            for (int i = 0; i < 2 * (sg.i1 - sg.i0) && ok; ++i, ++q.ring) {
+                                ok = wait_full(q.ring);
+                                if (ok) arrive(empty(q.ring % STAGES));
+                            }
+                            arrive(seg_empty(q.seg % SEGS));
+                            ++q.seg;
+                            v.seg = q.seg;
+                            v.ring = q.ring;
+                            if (!ok) break;
+                            continue;
+                        }
+                        enter(q, sg);
+                        ok = wait(q_full, (q.seg - 1) & 1);
+                        if (!ok) break;
                     }
-                    continue;
-                }
-                const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
-                const int TP = ceil_div(P, TN);
-                auto halves = [&](int i) { return tile_keys(sg.i0 + i, P, TP, p.R) > TH ? 2 : 1; };
-                int qi = 0, qh = 0, pi = 0, ph = 0;  // next half of S, of PV: tile of the segment and half of the tile
-                auto issue_s = [&]() {
-                    const int st = (it + 2 * qi) % STAGES, buf = uq & 1;
-                    if (qh == 0 && !wait_full(it + 2 * qi)) return false;
-                    if (one) issue_qk<D>(s_col + buf * TH, dq, dk + st * kS + qh * kHalf, id_qk);
-                    commit(s_full(t, buf));
-                    ++uq;
-                    if (++qh == halves(qi)) {
+                    if (busy >> q.h & 1) break;  // (a tile of one half, and the next one's first)
+                    const int st = q.ring % STAGES;
+                    if (q.h == 0) {
+                        ok = wait_full(q.ring);
+                        if (!ok) break;
+                    }
+                    if (one) issue_qk<D>(s_col + q.h * TH, dq, dk + st * kS + q.h * kHalf, id_qk);
+                    commit(s_full(t, q.h));
+                    busy |= 1u << q.h;
+                    if (++q.h == halves(q)) {
                         commit(empty(st));
-                        qh = 0;
-                        if (++qi == nk) commit(q_empty);
+                        q.h = 0;
+                        q.ring += 2;
+                        if (++q.i == q.last) {
+                            commit(q_empty);
+                            q.in = false;
+                        }
                     }
-                    return true;
-                };
-                ok = issue_s();
-                if (ok && qi < nk) ok = issue_s();
-                for (bool first = true; ok && pi < nk; first = false) {
-                    const int vi = it + 2 * pi + 1, st = vi % STAGES, buf = up & 1;
-                    ok = ph > 0 || wait_full(vi);
-                    if (ok && first && ns > 0) ok = tc::mbar_wait(o_free(t), (ns - 1) & 1, abort_flag, wl);
-                    ok = ok && tc::mbar_wait(p_full(t, buf), (up >> 1) & 1, abort_flag, wl);
+                }
+                if (!ok || !busy) break;
+                // PV of the oldest half whose S is out
+                if (!v.in) {
+                    Segment sg;
+                    ok = read(v, sg);
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    if (one) issue_pv(o_col, s_col + buf * TH, dv + st * kS + ph * kHalf, id_pv, !first);
-                    commit(pv_done(t, buf));
-                    ++up;
-                    if (++ph == halves(pi)) {
-                        commit(empty(st));
-                        ph = 0;
-                        if (++pi == nk) commit(o_full(t));
-                    }
-                    if (qi < nk) ok = issue_s();
+                    arrive(seg_empty(v.seg % SEGS));
+                    enter(v, sg);
+                    if (ns++ > 0) ok = wait(o_free(t), ns & 1);  // (the record before has been read)
                 }
-                it += 2 * nk;
-                ++ns;
+                const int vi = v.ring + 1, st = vi % STAGES, h = v.h;
+                if (ok && h == 0) ok = wait_full(vi);
+                ok = ok && wait(p_full(t, h), pph >> h & 1);
+                if (!ok) break;
+                pph ^= 1u << h;
+                tc::fence_after_sync();
+                if (one) issue_pv(o_col, s_col + h * TH, dv + st * kS + h * kHalf, id_pv, v.i > v.first || h > 0);
+                commit(pv_done(t, h));
+                busy &= ~(1u << h);
+                if (++v.h == halves(v)) {
+                    commit(empty(st));
+                    v.h = 0;
+                    v.ring += 2;
+                    if (++v.i == v.last) {
+                        commit(o_full(t));
+                        v.in = false;
+                    }
+                }
             }
             commit(fin(t));  // every MMA completes before TMEM is freed
-            tc::mbar_wait_drain(fin(t), 0, wl);
+            if (one) tc::mbar_wait_drain(fin(t), 0, wl);
             __syncwarp();
         }
         __syncwarp();
@@ -603,14 +693,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t s_col = tbase + lane_off + t * 128, o_col = tbase + lane_off + 256 + t * D;
         const float sl2 = p.scale_log2;
         Segment sg;
-        int ring = 0, n_s = 0, n_seg = 0;
+        int ring = 0, n_seg = 0;
+        uint32_t ph = 0;  // phases of s_full (bits 0, 1: S buffers) and of pv_done (bits 2, 3)
         bool ok = true;
         while (next(sg, true)) {
             const int nk = sg.i1 - sg.i0, ring0 = ring;
             ring += 2 * nk;
             if (t >= sg.nt) continue;
-            const int P = sg.b < 0 ? S : p.prefix_len[sg.b];
-            const int TP = ceil_div(P, TN);
+            const int P = sg.len, TP = ceil_div(P, TN);
             const int r = sg.row0 + t * g.RT + rr;  // row of the sequence, or of the batch (shared)
             const bool valid = rr < g.RT && r < (sg.b < 0 ? p.B * p.R : p.R);
             const bool work = __any_sync(0xffffffffu, valid);
@@ -623,79 +713,78 @@ __global__ void __launch_bounds__(THREADS, 1)
                 vis_ghi = vis_glo + p.k;
             }
             float m_run = -INFINITY, l_run = 0.f;
-            for (int i = 0; i < nk && ok; ++i) {
+            int prev = -1;      // S buffer of the half before (-1: none in this segment)
+            bool fresh = true;  // some row of the warp has seen no key yet
+            auto wait_s = [&](int h) {
+                const uint32_t sp = ph >> h & 1;
+                if (!__all_sync(0xffffffffu, tc::mbar_try_wait(s_full(t, h), sp)))  // (TMEM accesses are warp-wide)
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(s_full(t, h), sp, abort_flag, wl));
+                ph ^= 1u << h;
+                if (prev >= 0) ph ^= 4u << prev;  // (counts the PV of the half before: the phase that half's P began)
+                return ok;
+            };
+            // Exponentials of a half against the running max as it stands: a stale one is exact as long as the weights
+            // fit, whatever their size, so no maximum is taken while their sum stays below 2^16.
+            auto softmax = [&](int h, bool masked, int lo, int glo, int ghi) {
+                const uint32_t sc = s_col + h * TH;
+                float lt = 0.f;
+                bool again = fresh;
+                for (int tries = 0;; again = true) {
+                    if (again) {
+                        const RowState st = raise_max<D>(sc, h * TH, lo, glo, ghi, sl2, lt, m_run, l_run, o_col,
+                                                         pv_done(t, max(prev, 0)), (ph >> (2 + max(prev, 0)) & 1) ^ 1u, abort_flag);
+                        m_run = st.m;
+                        l_run = st.l;
+                        ok = st.ok;
+                        if (!ok) return;
+                        fresh = __any_sync(0xffffffffu, m_run == -INFINITY);
+                    }
+                    uint32_t u[2][32], pk[32];
+                    load_scores(sc, u);
+                    if (masked) mask_scores(u, h * TH, lo, glo, ghi);
+                    lt = half_exp(u, sl2, m_run == -INFINITY ? 0.f : -m_run, pk);
+                    if (__all_sync(0xffffffffu, lt < 65536.f) || tries++ > 0) {
+                        tc::tmem_st32(sc, pk);
+                        break;
+                    }
+                }
+                l_run += lt;
+            };
+            auto hand_over = [&](int h) {
+                prev = h;
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(p_full(t, h));
+            };
+            // whole tiles of cached keys: nothing masked.  (A loop of its own, its halves unrolled: 462 k cycles against
+            // 537 k for the largest shapes below.)
+            const int whole = work ? min(sg.i1, P / TN) - sg.i0 : 0;
+            int i = 0;
+            for (; i < whole && ok; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_s(h)) break;
+                    softmax(h, false, TN, 0, 0);
+                    if (!ok) break;
+                    hand_over(h);
+                }
+            }
+            // the others
+            for (; i < nk && ok; ++i) {
                 const int kt = sg.i0 + i, keys = tile_keys(kt, P, TP, p.R);
                 const int nh = keys > TH ? 2 : 1;
-                for (int h = 0; h < nh; ++h, ++n_s) {
-                    const int buf = n_s & 1;
-                    const uint32_t sc = s_col + buf * TH;
-                    bool have = tc::mbar_wait(s_full(t, buf), (n_s >> 1) & 1, abort_flag, wl);
-                    ok = __all_sync(0xffffffffu, have);  // TMEM accesses are warp-collective
-                    if (!ok) break;
-                    if (work) {
-                        tc::fence_after_sync();
-                        uint32_t u[2][32];
-                        tc::tmem_ld32(sc, u[0]);
-                        tc::tmem_ld32(sc + 32, u[1]);
-                        tc::tmem_wait_ld();
-                        const bool masked = kt >= TP || keys < TH * nh;
-                        if (masked) {  // by select, so that masked scores may be anything
-                            int lo = keys, glo = 0, ghi = 0;
-                            if (kt >= TP) {
-                                const int nn0 = (kt - TP) * TN;
-                                lo = min(vis_lim - nn0, keys);
-                                glo = vis_glo - nn0;
-                                ghi = min(vis_ghi - nn0, keys);
-                            }
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int k0 = h * TH + c * 32;
-                                const uint32_t bits = range_bits(0, lo, k0) | range_bits(glo, ghi, k0);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) u[c][j] = (bits >> j) & 1u ? u[c][j] : 0xff800000u;
-                            }
-                        }
-                        // Exponentials against the running max as it stands: a stale one is exact as long as the weights
-                        // fit, whatever their size, so no maximum is taken while their sum stays below 2^16.  Above it
-                        // (a score 2^10 to 2^16 times the running max's weight, or one that is not finite) the max is
-                        // raised and the half done again.  Rows with no visible key so far take their maximum first.
-                        if (__any_sync(0xffffffffu, m_run == -INFINITY)) {
-                            const float mx = half_max(u) * sl2;
-                            if (m_run == -INFINITY && mx > -INFINITY) m_run = mx;
-                        }
-                        float lt;
-                        while (true) {
-                            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-                            lt = masked ? half_exp<false>(sc, u, sl2, neg_m) : half_exp<true>(sc, u, sl2, neg_m);
-                            if (__all_sync(0xffffffffu, lt < 65536.f)) break;
-                            const float mx = half_max(u) * sl2;
-                            const bool grow = mx > m_run && !(lt < 65536.f) && mx < INFINITY;
-                            if (!(mx < INFINITY)) lt = l_run = __int_as_float(0x7fffffff);  // no softmax of such scores
-                            if (!__any_sync(0xffffffffu, grow)) break;
-                            // O is at rest once the last half's PV has completed: the next one awaits this P
-                            if (i + h > 0) {
-                                const bool got = tc::mbar_wait(pv_done(t, buf ^ 1), ((n_s - 1) >> 1) & 1, abort_flag, wl);
-                                ok = __all_sync(0xffffffffu, got);
-                                if (!ok) break;
-                                tc::fence_after_sync();
-                                const float f = grow ? fast_exp2(m_run - mx) : 1.f;
-                                l_run *= f;
+                int lo = keys, glo = 0, ghi = 0;
+                if (kt >= TP) {
+                    const int nn0 = (kt - TP) * TN;
+                    lo = min(vis_lim - nn0, keys);
+                    glo = vis_glo - nn0;
+                    ghi = min(vis_ghi - nn0, keys);
+                }
 #pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
-                                    uint32_t v[32];
-                                    tc::tmem_ld32(o_col + c * 32, v);
-                                    tc::tmem_wait_ld();
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                                    tc::tmem_st32(o_col + c * 32, v);
-                                }
-                            }
-                            if (grow) m_run = mx;
-                            tc::tmem_wait_st();  // the redone P overwrites the first pass's
-                        }
-                        if (!ok) break;
-                        l_run += lt;
-                    }
+                for (int h = 0; h < nh; ++h) {
+                    if (!wait_s(h)) break;
+                    if (work) softmax(h, true, lo, glo, ghi);
+                    if (!ok) break;
                     if (h == nh - 1 && keys < TH * nh) {
                         // keys past the end: zero their V rows (0 * garbage could be NaN) before this row tile's PV
                         // reads them (with two row tiles both do)
@@ -711,9 +800,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         tc::fence_proxy_async_smem();
                     }
-                    tc::tmem_wait_st();
-                    tc::fence_before_sync();
-                    tc::mbar_arrive(p_full(t, buf));
+                    hand_over(h);
                 }
             }
             tc::tmem_wait_st();
@@ -722,6 +809,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = __all_sync(0xffffffffu, got);
             if (!ok) break;
             ++n_seg;
+            if (prev >= 0) ph ^= 4u << prev;
             if (work) {
                 tc::fence_after_sync();
                 uint32_t v[D / 32][32];
@@ -763,10 +851,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0 && *abort_flag) atomicOr(p.dev_status, TIDAR_DEV_TIMEOUT);
 }
 
-// Joins the records of 32 rows (lane = row) of one KV head; warp w has columns [8w, 8w + 8).  Also reports lengths and
-// pages out of range and leaves those rows alone.
+// Joins the records of 32 rows (lane = row) of one KV head; warp w has columns [8w, 8w + 8).  A row has as many records
+// as CTAs worked on its two blocks; their headers are read all at once (one warp per record), then their values eight at
+// a time, in the order of the line.  Also reports lengths and pages out of range and leaves those rows alone.
+constexpr int kHeads = 64;  // records whose headers are held at a time
 template <int D>
 __global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p) {
+    constexpr int WARPS = D / 8;
+    __shared__ float2 heads[kHeads][32];
     __shared__ int bad_seq[32];
     const int lane = threadIdx.x & 31, chunk = threadIdx.x >> 5;
     const int kvh = blockIdx.y;
@@ -776,15 +868,28 @@ __global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p
     const int per_seq = p.R * p.G;
     const int b = (int)min(m / per_seq, (long)p.B - 1);
     const int mr = (int)(m - (long)b * per_seq), r = mr / p.G, gq = mr - r * p.G;
+    // the two blocks that hold this row: shared (x = 0) and own (x = 1)
+    const int sr = b * p.R + r, st = sr / g.RT, ot = r / g.RT;
+    const int id[2] = {kvh * g.blocks + st / 2, kvh * g.blocks + g.shared_blocks + b * g.own_blocks + ot / 2};
+    const int row[2] = {(sr - st * g.RT) * p.G + gq, (r - ot * g.RT) * p.G + gq};
+    if (threadIdx.x < 32) bad_seq[lane] = 0;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const bool in = m < rows;
     const int S = p.shared_len[0], P = p.prefix_len[b];
+    int2 c[2] = {make_int2(0, -1), make_int2(0, -1)};
+    if (in) {
+        c[0] = reinterpret_cast<const int2 *>(p.ws)[id[0]];
+        c[1] = reinterpret_cast<const int2 *>(p.ws)[id[1]];
+    }
     int bits = (S < 0 || S > p.S_max || P < 0 || P > p.P_max) ? TIDAR_DEV_BAD_PREFIX : 0;
     if (p.block_table) {
-        const bool s_ok = S >= 0 && S <= p.S_max;
-        if (s_ok && block_bad_page(p.shared_table, S, p.num_pages)) bits |= TIDAR_DEV_BAD_PAGE;
-        if (threadIdx.x < 32) bad_seq[lane] = 0;
-        __syncthreads();
+        int bad = 0;
+        if (S >= 0 && S <= p.S_max)
+            for (int i = threadIdx.x; i < ceil_div(S, kPageRows); i += blockDim.x) {
+                const int pg = p.shared_table[i];
+                bad |= pg < 0 || pg >= p.num_pages;
+            }
         // (at most 32 rows: the sequences of the block's first to last row)
         const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 31);
         for (int s = b0; s <= b1; ++s) {
@@ -795,55 +900,64 @@ __global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p
                 if (pg < 0 || pg >= p.num_pages) bad_seq[s - b0] = 1;
             }
         }
-        __syncthreads();
-        if (bad_seq[b - b0]) bits |= TIDAR_DEV_BAD_PAGE;
+        if (__syncthreads_or(bad) || bad_seq[b - b0]) bits |= TIDAR_DEV_BAD_PAGE;
     }
-    if (m >= rows) return;
-    if (bits) {
-        if (chunk == 0) atomicOr(p.dev_status, bits);
-        return;
-    }
-    // the two blocks that hold this row: shared (x = 0) and own (x = 1)
-    const int sr = b * p.R + r, st = sr / g.RT, ot = r / g.RT;
-    const int id[2] = {kvh * g.blocks + st / 2, kvh * g.blocks + g.shared_blocks + b * g.own_blocks + ot / 2};
-    const int row[2] = {(sr - st * g.RT) * p.G + gq, (r - ot * g.RT) * p.G + gq};
+    if (bits && in && chunk == 0) atomicOr(p.dev_status, bits);
     const size_t rec_bytes = tile_record_bytes(D);
     const uint8_t *recs = p.ws + info_bytes((size_t)p.Hkv * g.blocks);
+    int n0 = 0, n = 0;  // records: shared ones, all
     const uint8_t *rec[2];
-    int count[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int2 c = x == 0 && S == 0 ? make_int2(0, -1) : reinterpret_cast<const int2 *>(p.ws)[id[x]];
-        count[x] = c.y - c.x + 1;
-        rec[x] = recs + ((size_t)(c.x + id[x]) * 2 + ((x == 0 ? st : ot) & 1)) * rec_bytes;
+    if (in && !bits) {
+        n0 = S == 0 ? 0 : c[0].y - c[0].x + 1;
+        n = n0 + c[1].y - c[1].x + 1;
     }
-    float mx = -INFINITY;
-    // every record of the row, in the order of the line
-    auto each = [&](auto &&f) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            for (int c = 0; c < count[x]; ++c) f(rec[x] + c * 2 * rec_bytes, row[x]);
-    };
-    each([&](const uint8_t *rec, int rw) {
-        mx = fmaxf(mx, reinterpret_cast<const float2 *>(rec + TM * D * 2)[rw].x);
-    });
-    float acc[8], wsum = 0.f;
+    rec[0] = recs + ((size_t)(c[0].x + id[0]) * 2 + (st & 1)) * rec_bytes;
+    rec[1] = recs + ((size_t)(c[1].x + id[1]) * 2 + (ot & 1)) * rec_bytes;
+    auto record = [&](int i) { return i < n0 ? rec[0] + (size_t)i * 2 * rec_bytes : rec[1] + (size_t)(i - n0) * 2 * rec_bytes; };
+    const int nmax = __reduce_max_sync(0xffffffffu, n);  // (every warp has the same rows)
+    float mx = -INFINITY, wsum = 0.f, acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    each([&](const uint8_t *rec, int rw) {
-        const float2 hd = reinterpret_cast<const float2 *>(rec + TM * D * 2)[rw];
-        const uint4 raw = reinterpret_cast<const uint4 *>(rec)[chunk * TM + rw];
-        const float w = hd.x == -INFINITY ? 0.f : fast_exp2(hd.x - mx);
-        wsum += w;
-        const float f = w * hd.y;
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    for (int h0 = 0; h0 < nmax; h0 += kHeads) {
+        const int nh = min(kHeads, nmax - h0);
+        if (h0 > 0) __syncthreads();
+#pragma unroll 4
+        for (int i = chunk; i < nh; i += WARPS)
+            heads[i][lane] = h0 + i < n ? reinterpret_cast<const float2 *>(record(h0 + i) + TM * D * 2)[row[h0 + i < n0 ? 0 : 1]]
+                                        : make_float2(-INFINITY, 0.f);
+        __syncthreads();
+        float top = mx;
+#pragma unroll 4
+        for (int i = 0; i < nh; ++i) top = fmaxf(top, heads[i][lane].x);
+        const float keep = mx == -INFINITY ? 0.f : fast_exp2(mx - top);
+        wsum *= keep;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 v = unpack_half2(u[e]);
-            acc[2 * e] = fmaf(f, v.x, acc[2 * e]);
-            acc[2 * e + 1] = fmaf(f, v.y, acc[2 * e + 1]);
+        for (int e = 0; e < 8; ++e) acc[e] *= keep;
+        mx = top;
+        for (int i0 = 0; i0 < nh; i0 += 8) {
+            uint4 raw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (h0 + i0 + i < n && i0 + i < nh)
+                    raw[i] = reinterpret_cast<const uint4 *>(record(h0 + i0 + i))[chunk * TM + row[h0 + i0 + i < n0 ? 0 : 1]];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!(h0 + i0 + i < n && i0 + i < nh)) continue;
+                const float2 hd = heads[i0 + i][lane];
+                const float w = hd.x == -INFINITY ? 0.f : fast_exp2(hd.x - mx);
+                wsum += w;
+                const float f = w * hd.y;
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = unpack_half2(u[e]);
+                    acc[2 * e] = fmaf(f, v.x, acc[2 * e]);
+                    acc[2 * e + 1] = fmaf(f, v.y, acc[2 * e + 1]);
+                }
+            }
         }
-    });
+    }
+    if (n == 0) return;
     const float inv = 1.f / wsum;
     const size_t orow = ((size_t)b * p.R + r) * p.Hq + kvh * p.G + gq;
     *reinterpret_cast<uint4 *>(p.out + orow * D + chunk * 8) =
@@ -930,6 +1044,14 @@ cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool shared_attn_fits(int B, int R, int Hkv, int G, int S_max, int P_max) {
+    const Geometry g = geometry(B, R, G);
+    const long long own = (long long)ceil_div(P_max, TN) + ceil_div(R, TN);
+    const long long cost = (long long)g.shared_blocks * (kCostBlock + (long long)ceil_div(S_max, TN) * kCostPair) +
+                           (long long)B * g.own_blocks * (kCostBlock + own * kCostPair);
+    return cost * Hkv < (1LL << 31);
+}
 
 size_t shared_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int R, int, int) {
     const Geometry g = geometry(B, R, Hq / Hkv);
