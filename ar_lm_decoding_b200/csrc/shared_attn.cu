@@ -55,8 +55,9 @@ struct Line {
 };
 
 __host__ __device__ __forceinline__ int rows_per_tile(int G) { return TM / G; }
-// The workspace: (first, last) CTA of every block, then the records.
-__host__ __device__ __forceinline__ size_t info_bytes(size_t blocks) { return align256(blocks * 8); }
+// The workspace: (first, last) CTA of every block, whether a sequence's pages (and, last, the shared ones) are all in
+// range, then the records.
+__host__ __device__ __forceinline__ size_t info_bytes(size_t blocks, int B) { return align256(blocks * 8 + (size_t)B * 4 + 4); }
 // One record: two row tiles, each [D/8 chunks][128 rows] 16-byte chunks of 8 fp16 and a header [128 rows] (log2 of the
 // row's sum, scale of its values).
 __host__ __device__ __forceinline__ size_t tile_record_bytes(int D) { return (size_t)TM * (D * 2 + 8); }
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::fence_after_sync();
     const uint32_t tbase = *tmem_slot;
     const int cta = blockIdx.x;
-    const size_t info = info_bytes((size_t)p.Hkv * g.blocks);
+    const size_t info = info_bytes((size_t)p.Hkv * g.blocks, p.B);
     const long long wl = kWaitCycles;
 
     // The next segment for the calling thread (`all`: for its whole warp, which calls it together).
@@ -471,6 +472,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         return sg.nt > 0;
     };
 
+    if (p.block_table && warp == 3) {  // every CTA looks over some of the page tables, for combine_kernel
+        int *bad_pages = reinterpret_cast<int *>(reinterpret_cast<int2 *>(p.ws) + (size_t)p.Hkv * g.blocks);
+        for (int b = (int)gridDim.x - 1 - cta; b <= p.B; b += gridDim.x) {
+            const int n = b < p.B ? p.prefix_len[b] : S;
+            const int32_t *pages = b < p.B ? p.block_table + (size_t)b * p.max_pages : p.shared_table;
+            bool bad = false;
+            for (int i = lane; i < ceil_div(min(max(n, 0), b < p.B ? p.P_max : p.S_max), kPageRows); i += 32)
+                bad |= pages[i] < 0 || pages[i] >= p.num_pages;
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) bad_pages[b] = bad;
+        }
+    }
     if (warp < 4) {
         Segment sg;
         if (warp == 2 && lane == 0) {
@@ -851,19 +864,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0 && *abort_flag) atomicOr(p.dev_status, TIDAR_DEV_TIMEOUT);
 }
 
-// Joins the records of 32 rows (lane = row) of one KV head; warp w has columns [8w, 8w + 8).  A row has as many records
-// as CTAs worked on its two blocks; their headers are read all at once (one warp per record), then their values eight at
-// a time, in the order of the line.  Also reports lengths and pages out of range and leaves those rows alone.
+// Joins the records of kJoin rows of one KV head; a thread has 16 columns of one row.  A row has as many
+// records as CTAs worked on its two blocks; their headers are read all at once (a group of threads per record), their values four
+// at a time (the first four beside the headers), in the order of the line.  Also reports lengths and pages out of range and
+// leaves those rows alone.
 constexpr int kHeads = 64;  // records whose headers are held at a time
+constexpr int kJoin = 16;   // rows of a CTA
 template <int D>
-__global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p) {
-    constexpr int WARPS = D / 8;
-    __shared__ float2 heads[kHeads][32];
-    __shared__ int bad_seq[32];
-    const int lane = threadIdx.x & 31, chunk = threadIdx.x >> 5;
+__global__ void __launch_bounds__(D / 16 * kJoin) combine_kernel(const SharedAttnParams p) {
+    constexpr int GROUPS = D / 16, U = 4;
+    __shared__ float2 heads[kHeads][kJoin];
+    const int lane = threadIdx.x % kJoin, chunk = threadIdx.x / kJoin;
     const int kvh = blockIdx.y;
     const long rows = (long)p.B * p.R * p.G;
-    const long m = (long)blockIdx.x * 32 + lane;
+    const long m = (long)blockIdx.x * kJoin + lane;
     const Geometry g = geometry(p.B, p.R, p.G);
     const int per_seq = p.R * p.G;
     const int b = (int)min(m / per_seq, (long)p.B - 1);
@@ -872,87 +886,87 @@ __global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p
     const int sr = b * p.R + r, st = sr / g.RT, ot = r / g.RT;
     const int id[2] = {kvh * g.blocks + st / 2, kvh * g.blocks + g.shared_blocks + b * g.own_blocks + ot / 2};
     const int row[2] = {(sr - st * g.RT) * p.G + gq, (r - ot * g.RT) * p.G + gq};
-    if (threadIdx.x < 32) bad_seq[lane] = 0;
+    const bool in = m < rows;
+    const int2 *ctas = reinterpret_cast<const int2 *>(p.ws);
+    const int *bad_pages = reinterpret_cast<const int *>(ctas + (size_t)p.Hkv * g.blocks);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const bool in = m < rows;
     const int S = p.shared_len[0], P = p.prefix_len[b];
     int2 c[2] = {make_int2(0, -1), make_int2(0, -1)};
+    int pages = 0;
     if (in) {
-        c[0] = reinterpret_cast<const int2 *>(p.ws)[id[0]];
-        c[1] = reinterpret_cast<const int2 *>(p.ws)[id[1]];
+        c[0] = ctas[id[0]];
+        c[1] = ctas[id[1]];
+        if (p.block_table) pages = bad_pages[b] | bad_pages[p.B];
     }
     int bits = (S < 0 || S > p.S_max || P < 0 || P > p.P_max) ? TIDAR_DEV_BAD_PREFIX : 0;
-    if (p.block_table) {
-        int bad = 0;
-        if (S >= 0 && S <= p.S_max)
-            for (int i = threadIdx.x; i < ceil_div(S, kPageRows); i += blockDim.x) {
-                const int pg = p.shared_table[i];
-                bad |= pg < 0 || pg >= p.num_pages;
-            }
-        // (at most 32 rows: the sequences of the block's first to last row)
-        const int b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 31);
-        for (int s = b0; s <= b1; ++s) {
-            const int n = p.prefix_len[s];
-            if (n < 0 || n > p.P_max) continue;
-            for (int i = threadIdx.x; i < ceil_div(n, kPageRows); i += blockDim.x) {
-                const int pg = p.block_table[(size_t)s * p.max_pages + i];
-                if (pg < 0 || pg >= p.num_pages) bad_seq[s - b0] = 1;
-            }
-        }
-        if (__syncthreads_or(bad) || bad_seq[b - b0]) bits |= TIDAR_DEV_BAD_PAGE;
-    }
+    if (pages) bits |= TIDAR_DEV_BAD_PAGE;
     if (bits && in && chunk == 0) atomicOr(p.dev_status, bits);
+    if (S == 0) c[0] = make_int2(0, -1);
+    // (a launch whose waits ran out may have left these unset: it has reported that)
+    auto sound = [](int2 v) { return v.x >= 0 && v.y < kNumSMs && v.x <= v.y + 1; };
+    const bool go = in && !bits && sound(c[0]) && sound(c[1]);
+    const int n0 = go ? c[0].y - c[0].x + 1 : 0;          // records: shared ones,
+    const int n = go ? n0 + c[1].y - c[1].x + 1 : 0;      // all
     const size_t rec_bytes = tile_record_bytes(D);
-    const uint8_t *recs = p.ws + info_bytes((size_t)p.Hkv * g.blocks);
-    int n0 = 0, n = 0;  // records: shared ones, all
-    const uint8_t *rec[2];
-    if (in && !bits) {
-        n0 = S == 0 ? 0 : c[0].y - c[0].x + 1;
-        n = n0 + c[1].y - c[1].x + 1;
-    }
-    rec[0] = recs + ((size_t)(c[0].x + id[0]) * 2 + (st & 1)) * rec_bytes;
-    rec[1] = recs + ((size_t)(c[1].x + id[1]) * 2 + (ot & 1)) * rec_bytes;
-    auto record = [&](int i) { return i < n0 ? rec[0] + (size_t)i * 2 * rec_bytes : rec[1] + (size_t)(i - n0) * 2 * rec_bytes; };
-    const int nmax = __reduce_max_sync(0xffffffffu, n);  // (every warp has the same rows)
-    float mx = -INFINITY, wsum = 0.f, acc[8];
+    const uint8_t *recs = p.ws + info_bytes((size_t)p.Hkv * g.blocks, p.B);
+    const uint8_t *rec0 = recs + ((size_t)(c[0].x + id[0]) * 2 + (st & 1)) * rec_bytes;
+    const uint8_t *rec1 = recs + ((size_t)(c[1].x + id[1]) * 2 + (ot & 1)) * rec_bytes - (size_t)n0 * 2 * rec_bytes;
+    auto values = [&](int i, uint4 (&v)[2]) {
+        const bool sh = i < n0;
+        const uint4 *x = reinterpret_cast<const uint4 *>((sh ? rec0 : rec1) + (size_t)i * 2 * rec_bytes) + 2 * chunk * TM +
+                         (sh ? row[0] : row[1]);
+        v[0] = x[0];
+        v[1] = x[TM];
+    };
+    auto head = [&](int i) {
+        const bool sh = i < n0;
+        return reinterpret_cast<const float2 *>((sh ? rec0 : rec1) + (size_t)i * 2 * rec_bytes + TM * D * 2)[sh ? row[0] : row[1]];
+    };
+    const int nmax = __reduce_max_sync(0xffffffffu, n);  // (every warp has the same rows once or twice)
+    float mx = -INFINITY, wsum = 0.f, acc[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
     for (int h0 = 0; h0 < nmax; h0 += kHeads) {
         const int nh = min(kHeads, nmax - h0);
+        uint4 raw[U][2];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (h0 + i < n) values(h0 + i, raw[i]);
         if (h0 > 0) __syncthreads();
 #pragma unroll 4
-        for (int i = chunk; i < nh; i += WARPS)
-            heads[i][lane] = h0 + i < n ? reinterpret_cast<const float2 *>(record(h0 + i) + TM * D * 2)[row[h0 + i < n0 ? 0 : 1]]
-                                        : make_float2(-INFINITY, 0.f);
+        for (int i = chunk; i < nh; i += GROUPS) heads[i][lane] = h0 + i < n ? head(h0 + i) : make_float2(-INFINITY, 0.f);
         __syncthreads();
         float top = mx;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < nh; ++i) top = fmaxf(top, heads[i][lane].x);
         const float keep = mx == -INFINITY ? 0.f : fast_exp2(mx - top);
         wsum *= keep;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] *= keep;
+        for (int e = 0; e < 16; ++e) acc[e] *= keep;
         mx = top;
-        for (int i0 = 0; i0 < nh; i0 += 8) {
-            uint4 raw[8];
+        for (int i0 = 0; i0 < nh; i0 += U) {
+            if (i0 > 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (h0 + i0 + i < n && i0 + i < nh)
-                    raw[i] = reinterpret_cast<const uint4 *>(record(h0 + i0 + i))[chunk * TM + row[h0 + i0 + i < n0 ? 0 : 1]];
+                for (int i = 0; i < U; ++i)
+                    if (i0 + i < nh && h0 + i0 + i < n) values(h0 + i0 + i, raw[i]);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!(h0 + i0 + i < n && i0 + i < nh)) continue;
+            for (int i = 0; i < U; ++i) {
+                if (!(i0 + i < nh && h0 + i0 + i < n)) continue;
                 const float2 hd = heads[i0 + i][lane];
                 const float w = hd.x == -INFINITY ? 0.f : fast_exp2(hd.x - mx);
                 wsum += w;
                 const float f = w * hd.y;
-                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = unpack_half2(u[e]);
-                    acc[2 * e] = fmaf(f, v.x, acc[2 * e]);
-                    acc[2 * e + 1] = fmaf(f, v.y, acc[2 * e + 1]);
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t u[4] = {raw[i][x].x, raw[i][x].y, raw[i][x].z, raw[i][x].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = unpack_half2(u[e]);
+                        acc[8 * x + 2 * e] = fmaf(f, v.x, acc[8 * x + 2 * e]);
+                        acc[8 * x + 2 * e + 1] = fmaf(f, v.y, acc[8 * x + 2 * e + 1]);
+                    }
                 }
             }
         }
@@ -960,9 +974,13 @@ __global__ void __launch_bounds__(D * 4) combine_kernel(const SharedAttnParams p
     if (n == 0) return;
     const float inv = 1.f / wsum;
     const size_t orow = ((size_t)b * p.R + r) * p.Hq + kvh * p.G + gq;
-    *reinterpret_cast<uint4 *>(p.out + orow * D + chunk * 8) =
-        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const float *a = acc + 8 * x;
+        reinterpret_cast<uint4 *>(p.out + orow * D)[2 * chunk + x] =
+            make_uint4(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv),
+                       pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
+    }
     if (chunk == 0 && p.lse) p.lse[orow] = (mx + __log2f(wsum)) * kLn2;
 }
 
@@ -1035,8 +1053,8 @@ cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, shared_attn_kernel<D>, p, mp);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.R * p.G + 31) / 32), p.Hkv, 1);
-    cfg.blockDim = dim3(D * 4, 1, 1);
+    cfg.gridDim = dim3((unsigned)(((long long)p.B * p.R * p.G + kJoin - 1) / kJoin), p.Hkv, 1);
+    cfg.blockDim = dim3(D / 16 * kJoin, 1, 1);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, p);
     if (e != cudaSuccess) return e;
@@ -1056,7 +1074,7 @@ bool shared_attn_fits(int B, int R, int Hkv, int G, int S_max, int P_max) {
 size_t shared_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int R, int, int) {
     const Geometry g = geometry(B, R, Hq / Hkv);
     // a segment's record is at cta + block: along the line both only grow, and one of them from segment to segment
-    return info_bytes((size_t)Hkv * g.blocks) + ((size_t)kNumSMs + (size_t)Hkv * g.blocks) * 2 * tile_record_bytes(D);
+    return info_bytes((size_t)Hkv * g.blocks, B) + ((size_t)kNumSMs + (size_t)Hkv * g.blocks) * 2 * tile_record_bytes(D);
 }
 
 cudaError_t shared_attn_launch(const SharedAttnParams &p, cudaStream_t s) {
