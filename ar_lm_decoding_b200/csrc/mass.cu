@@ -1,52 +1,476 @@
-// Attention mass of the cache rows: one warp per (layer, sequence, KV head, row), its weights summed over the queries.
+// Attention mass of the cache rows (sm_100a, tcgen05): w(n) = sum over the newest rows' queries q of 2^(q k_n scale' -
+// lse'), the column sums of the softmax, for all layers in one launch.
+//
+// The products are taken as S^T = K Q^T: 128 keys are the rows of a tile (the lanes of TMEM) and up to 128 queries its
+// columns, so that a key's weights are summed by one thread in a fixed order and written by it alone: no atomics, no
+// exchange.  A key tile feeds all its queries from one read of K; more than 128 queries take turns over the CTA's run of
+// key tiles (from L2), the later ones adding to the mass.
+//
+// Work: the key tiles of all (layer, sequence, KV head) form one line, cut into equal shares of cost, one per CTA (every
+// SM the same work, whatever the lengths).  The pointers of the layers are on the device, so K comes by cp.async into the
+// swizzled layout, not through tensor maps.
+//
+// A CTA (13 warps): warps 0-3 and 4-7 take the sums of every other key tile, warps 8-11 copy (K tiles through a ring of 4
+// to 8, Q through two buffers), warp 12 issues the MMAs into two TMEM buffers.
+//
+// Bound by the bytes of K up to about 175 queries per key (a tile's 32 KB take an SM's share of HBM as long as 128 x 175
+// exponentials its MUFU), by the exponentials above.
 #include "cache_ops.cuh"
+#include "tc.cuh"
 
 namespace tidar {
 
 namespace {
 
-__global__ void __launch_bounds__(256) mass_rows_kernel(const MassParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = p.D / 32;
-    const int b = blockIdx.y, l = blockIdx.z / p.Hkv, kvh = blockIdx.z % p.Hkv;
-    const int N = p.prefix_len[b], a = p.row_count ? p.row_count[b] : p.R;
-    int bits = 0;
-    if (N < 0 || N > p.P_max) bits = TIDAR_DEV_BAD_PREFIX;
-    else if (a < 0 || a > p.R || a > N) bits = TIDAR_DEV_BAD_ACCEPT;
-    else if (p.block_table && block_bad_page(p.block_table + (size_t)b * p.max_pages, N, p.num_pages))
-        bits = TIDAR_DEV_BAD_PAGE;
-    if (bits) {
-        if (threadIdx.x == 0) atomicOr(p.dev_status, bits);
-        return;
+constexpr int TM = 128;       // keys of a tile
+constexpr int TQ = 128;       // queries of a turn
+constexpr int THREADS = 416;
+constexpr int COPIERS = 128;  // threads of warps 8-11
+constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
+constexpr int kBytesCost = 176;                  // cost of a tile that is bound by its bytes, in queries
+constexpr int kSkip = 1 << 30;                   // in rows[b]: a page out of range
+
+template <int D>
+struct Smem {
+    static constexpr int K_TILE = TM * D * 2;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int Q_BUF = TQ * D * 2;
+    static constexpr int K_OFF = 2 * Q_BUF;
+    static constexpr int LSE_OFF = K_OFF + STAGES * K_TILE;  // float[2][TQ]: -lse in log2 units
+    static constexpr int BAR_OFF = LSE_OFF + 2 * TQ * 4;
+    // k_full[STAGES], k_empty[STAGES], q_full[2], q_empty[2], d_full[2], d_empty[2], fin
+    static constexpr int NBARS = 2 * STAGES + 9;
+    static constexpr int MISC_OFF = BAR_OFF + (NBARS * 8 + 15) / 16 * 16;
+    static constexpr int SEQ_OFF = MISC_OFF + 16;  // long long cum[B + 1], int tiles[B], int rows[B]
+    static int alloc(int B) { return SEQ_OFF + (B + 1) * 8 + B * 8 + 1024; }
+};
+static_assert(Smem<128>::SEQ_OFF + (kMaxBatchShared + 1) * 16 + 1024 <= 227 * 1024 &&
+                  Smem<64>::SEQ_OFF + (kMaxBatchShared + 1) * 16 + 1024 <= 227 * 1024,
+              "shared memory beyond 227 KB");
+
+__device__ __forceinline__ int tile_cost(int queries) { return min(max(queries, kBytesCost), 1 << 16); }
+
+// A run of key tiles [t0, t1) of one head, as a CTA works on it.
+struct Run {
+    int l, b, h, t0, t1;
+};
+
+// Walks a CTA's runs.  cum[b]: cost of one KV head's tiles of the sequences before b; the line goes layer by layer,
+// sequence by sequence, head by head.
+struct Walker {
+    const long long *cum;
+    const int *tiles, *rows;
+    int L, B, Hkv, G;
+    __device__ int cost_of(int seq) const { return tile_cost((rows[seq] & ~kSkip) * G); }
+    int l, b, h;
+    int t;             // first tile of the next run
+    long long pos, x1; // position of that tile, end of the share
+    __device__ void start(const MassParams &p, const long long *c, const int *ti, const int *ro, int cta, int n) {
+        cum = c;
+        tiles = ti;
+        rows = ro;
+        L = p.L;
+        B = p.B;
+        Hkv = p.Hkv;
+        G = p.G;
+        const long long layer = cum[B] * Hkv, total = layer * L;
+        auto cut = [&](int i) { return total / n * i + (total % n * i + n - 1) / n; };
+        pos = cut(cta);
+        x1 = cut(cta + 1);
+        l = b = h = t = 0;
+        if (pos >= x1) return;
+        l = (int)(pos / layer);
+        const long long in = pos - l * layer;
+        int lo = 0, hi = B;  // the sequence that holds the position
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] * Hkv <= in) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        const long long rest = in - cum[b] * Hkv, head = cum[b + 1] - cum[b];
+        const int cost = cost_of(b);
+        h = (int)(rest / head);
+        t = (int)((rest - h * head + cost - 1) / cost);  // the first tile that begins at or behind the cut
+        pos = l * layer + cum[b] * Hkv + h * head + (long long)t * cost;
     }
-    const bf16 *q = reinterpret_cast<const bf16 *>(p.qs[l]);
-    const bf16 *kc = reinterpret_cast<const bf16 *>(p.k_caches[l]);
-    const float *lse = p.lses[l];
-    float *mass = p.masses[l] + ((size_t)b * p.Hkv + kvh) * p.P_max;
-    for (int n = blockIdx.x * 8 + warp; n < N; n += gridDim.x * 8) {
-        size_t at = (((size_t)b * p.Hkv + kvh) * p.P_max + n) * p.D;
-        if (p.block_table)
-            at = (((size_t)p.block_table[(size_t)b * p.max_pages + n / kPageRows] * p.Hkv + kvh) * kPageRows +
-                  n % kPageRows) * p.D;
-        float k[4], w = 0.f;
-        for (int e = 0; e < per; ++e) k[e] = __bfloat162float(kc[at + lane * per + e]);
-        for (int j = max(0, n - (N - a)); j < a; ++j)
-            for (int g = 0; g < p.G; ++g) {
-                const size_t row = ((size_t)b * p.R + j) * p.Hq + kvh * p.G + g;
-                float s = 0.f;
-                for (int e = 0; e < per; ++e) s = fmaf(k[e], __bfloat162float(q[row * p.D + lane * per + e]), s);
-                for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                w += exp2f(fmaf(s, p.scale_log2, -lse[row] * kLog2e));
+    __device__ bool next(Run &r) {
+        while (pos < x1) {
+            const int n = tiles[b], cost = cost_of(b);
+            const long long left = (x1 - pos + cost - 1) / cost;
+            r = Run{l, b, h, t, (int)min((long long)n, t + left)};
+            pos += (long long)(n - t) * cost;
+            t = 0;
+            if (++h == Hkv) {
+                h = 0;
+                do {
+                    if (++b == B) {
+                        b = 0;
+                        ++l;
+                    }
+                } while (l < L && tiles[b] == 0);
             }
-        if (lane == 0) mass[n] = n < N - a ? p.decay * mass[n] + w : w;
+            if (r.t0 < r.t1) return true;
+        }
+        return false;
     }
+};
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool read) {  // zeros where it does not read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
+    using L = Smem<D>;
+    constexpr int STAGES = L::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem), sK = sbase + L::K_OFF, bar0 = sbase + L::BAR_OFF;
+    auto k_full = [&](int s) { return bar0 + 8u * s; };
+    auto k_empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto q_full = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
+    auto q_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * STAGES + 4 + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 6 + i); };
+    const uint32_t fin = bar0 + 8u * (2 * STAGES + 8);
+    float *nlse = reinterpret_cast<float *>(smem + L::LSE_OFF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
+    long long *cum = reinterpret_cast<long long *>(smem + L::SEQ_OFF);
+    int *tiles = reinterpret_cast<int *>(cum + p.B + 1), *rows = tiles + p.B;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long long wl = kWaitCycles;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            tc::mbar_init(k_full(s), COPIERS);
+            tc::mbar_init(k_empty(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(q_full(i), COPIERS);
+            tc::mbar_init(q_empty(i), 1 + 8);  // the MMAs and the summing warps (which read the LSEs)
+            tc::mbar_init(d_full(i), 1);
+            tc::mbar_init(d_empty(i), 128);
+        }
+        tc::mbar_init(fin, 1);
+        *abort_flag = 0;
+        tc::mbar_fence_init();
+    }
+    if (warp == 12) tc::tmem_alloc(smem_u32(tmem_slot), 256);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    // the line; a sequence whose length or row count is out of range has no tiles
+    if (warp == 0) {
+        long long sum = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int x = 0, a = 0;
+            if (b < p.B) {
+                const int N = p.prefix_len[b];
+                a = p.row_count ? p.row_count[b] : p.R;
+                int bits = 0;
+                if (N < 0 || N > p.P_max) bits = TIDAR_DEV_BAD_PREFIX;
+                else if (a < 0 || a > p.R || a > N) bits = TIDAR_DEV_BAD_ACCEPT;
+                if (bits && blockIdx.x == 0) atomicOr(p.dev_status, bits);
+                // (no rows: the sums only decay, below)
+                x = bits || a == 0 ? 0 : ceil_div(N, TM);
+                if (bits) a = 0;
+                tiles[b] = x;
+                rows[b] = a;
+            }
+            long long inc = (long long)x * tile_cost(a * p.G);
+            const long long own = inc;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (b < p.B) cum[b] = sum + inc - own;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) cum[p.B] = sum;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = *tmem_slot;
+    const int cta = blockIdx.x, ncta = gridDim.x;
+    Walker walk;
+    walk.start(p, cum, tiles, rows, cta, ncta);
+    // Paged caches: the CTA looks over the pages of the sequences of its share; one with a page out of range is skipped.
+    if (p.block_table && walk.pos < walk.x1) {
+        Walker end = walk;
+        Run r;
+        int b0 = p.B, b1 = -1, first = walk.l;
+        while (end.next(r)) {
+            if (r.l != first || b1 - b0 >= p.B) {  // (into another layer: every sequence, perhaps)
+                b0 = 0;
+                b1 = p.B - 1;
+                break;
+            }
+            b0 = min(b0, r.b);
+            b1 = max(b1, r.b);
+        }
+        for (int b = b0; b <= b1; ++b) {
+            if (tiles[b] == 0) continue;  // (uniform over the block)
+            if (block_bad_page(p.block_table + (size_t)b * p.max_pages, p.prefix_len[b], p.num_pages) && tid == 0) {
+                rows[b] |= kSkip;
+                atomicOr(p.dev_status, TIDAR_DEV_BAD_PAGE);
+            }
+        }
+        __syncthreads();
+    }
+    auto skipped = [&](const Run &r) { return (rows[r.b] & kSkip) != 0; };
+    auto turns = [&](int a) { return ceil_div(a * p.G, TQ); };
+
+    if (warp < 8) {
+        // ================= sums: warpgroup w takes every other tile; thread = key =================
+        const int w = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+        const uint32_t d_col = tbase + ((uint32_t)(q4 * 32) << 16) + w * TQ;
+        const uint64_t sl2 = pair(p.scale_log2, p.scale_log2);
+        int turn = 0, run = 0, taken = 0;  // turns, runs, this warpgroup's tiles
+        bool ok = true;
+        Run r;
+        while (ok && walk.next(r)) {
+            if (skipped(r)) continue;
+            const int t0 = r.t0 + ((run++ ^ w) & 1);  // (a key stays with its thread through the turns)
+            const int N = p.prefix_len[r.b], a = rows[r.b], nturn = turns(a);
+            float *mass = p.masses[r.l] + ((size_t)r.b * p.Hkv + r.h) * p.P_max;
+            for (int c = 0; c < nturn && ok; ++c, ++turn) {
+                const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ), chunks = ceil_div(nq, 32);
+                const float *nl = nlse + qb * TQ;
+                // (also without a tile: the arrival below is for this turn)
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(q_full(qb), (turn >> 1) & 1, abort_flag, wl));
+                for (int t = t0; t < r.t1 && ok; t += 2) {
+                    const int key = t * TM + row;
+                    const bool mine = key < N;
+                    float old = 0.f;
+                    if (mine && (c > 0 || key < N - a)) old = mass[key];
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(d_full(w), taken & 1, abort_flag, wl));
+                    if (!ok) break;  // (TMEM accesses are warp-wide)
+                    tc::fence_after_sync();
+                    ++taken;
+                    // a newest row n sees only itself and what follows: queries of rows j >= n - (N - a)
+                    const int cmin = max(0, (key - (N - a)) * p.G - c * TQ);
+                    const bool cut = t * TM + TM > N - a;
+                    uint64_t sum[4] = {0, 0, 0, 0};
+                    for (int x = 0; x < chunks; ++x) {
+                        uint32_t u[32];
+                        tc::tmem_ld32(d_col + x * 32, u);
+                        uint64_t nl2[16];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const ulonglong2 v = reinterpret_cast<const ulonglong2 *>(nl + x * 32)[j];
+                            nl2[2 * j] = v.x;
+                            nl2[2 * j + 1] = v.y;
+                        }
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float e, f;
+                            unpair(fma2(pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), sl2, nl2[j]), e, f);
+                            e = fast_exp2(e);
+                            f = fast_exp2(f);
+                            if (cut) {  // by select: a masked weight may be anything
+                                e = x * 32 + 2 * j >= cmin ? e : 0.f;
+                                f = x * 32 + 2 * j + 1 >= cmin ? f : 0.f;
+                            }
+                            sum[j & 3] = add2(sum[j & 3], pair(e, f));
+                        }
+                    }
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(d_empty(w));
+                    float e, f;
+                    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e, f);
+                    if (mine) mass[key] = c > 0 ? old + (e + f) : key < N - a ? fmaf(p.decay, old, e + f) : e + f;
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(q_empty(qb));
+            }
+        }
+        // sequences without new rows: their sums decay
+        if (p.decay != 1.f) {
+            const long heads = (long)p.L * p.B * p.Hkv;
+            for (long hd = cta; hd < heads; hd += ncta) {
+                const int h = (int)(hd % p.Hkv), b = (int)(hd / p.Hkv % p.B), l = (int)(hd / p.Hkv / p.B);
+                const int N = p.prefix_len[b];
+                if (N <= 0 || N > p.P_max || !p.row_count || p.row_count[b] != 0) continue;
+                float *mass = p.masses[l] + ((size_t)b * p.Hkv + h) * p.P_max;
+                for (int i = tid; i < N; i += 256) mass[i] *= p.decay;
+            }
+        }
+    } else if (warp < 12) {
+        // ================= copies =================
+        const int ct = tid - 256;
+        constexpr int CH = D / 8, RW = COPIERS / CH;  // 16-byte chunks of a row; rows of one sweep (a multiple of 8)
+        const int c16 = ct % CH, r0 = ct / CH;
+        const uint32_t dst0 = (c16 >> 3) * TM * 128 + r0 * 128 + (((c16 & 7) ^ (r0 & 7)) << 4);
+        int it = 0, turn = 0, landed = 0;  // K tiles issued, turns, K tiles whose landing has been announced
+        // Every K tile is one copy group, the Q of a turn part of its first tile's group: a tile is announced once at most
+        // STAGES - 2 younger groups are under way.
+        int q_of[2] = {-1, -1};  // per Q buffer: the tile whose group holds it
+        auto announce = [&](int upto) {
+            for (; landed < upto; ++landed) {
+                for (int i = 0; i < 2; ++i)
+                    if (q_of[i] == landed) tc::mbar_arrive(q_full(i));
+                tc::mbar_arrive(k_full(landed % STAGES));
+            }
+        };
+        bool ok = true;
+        Run r;
+        while (ok && walk.next(r)) {
+            if (skipped(r)) continue;
+            const int N = p.prefix_len[r.b], a = rows[r.b], nturn = turns(a);
+            const uint8_t *kc = static_cast<const uint8_t *>(p.k_caches[r.l]);
+            const uint8_t *q = static_cast<const uint8_t *>(p.qs[r.l]) + ((size_t)r.b * p.R * p.Hq + r.h * p.G) * D * 2;
+            const float *lse = p.lses[r.l] + (size_t)r.b * p.R * p.Hq + r.h * p.G;
+            for (int c = 0; c < nturn && ok; ++c, ++turn) {
+                const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ);
+                // (the buffer's last reader may still wait for tiles that are on their way: announce them first)
+                if (turn >= 2) {
+                    asm volatile("cp.async.wait_all;\n" ::: "memory");
+                    tc::fence_proxy_async_smem();
+                    announce(it);
+                    ok = tc::mbar_wait(q_empty(qb), ((turn >> 1) - 1) & 1, abort_flag, wl);
+                    if (!ok) break;
+                }
+                for (int x = r0; x < (nq + 31) / 32 * 32; x += RW) {
+                    const int i = c * TQ + x, j = i / p.G, gq = i - j * p.G;
+                    copy16(sbase + qb * L::Q_BUF + dst0 + (x - r0) * 128,
+                           q + ((size_t)j * p.Hq + gq) * (x < nq ? D * 2 : 0) + c16 * 16, x < nq);
+                }
+                {
+                    const int i = c * TQ + ct, j = i / p.G, gq = i - j * p.G;
+                    nlse[qb * TQ + ct] = ct < nq ? -lse[(size_t)j * p.Hq + gq] * kLog2e : -INFINITY;
+                }
+                q_of[qb] = it;
+                for (int t = r.t0; t < r.t1; ++t, ++it) {
+                    const int st = it % STAGES;
+                    if (it >= STAGES) {
+                        ok = tc::mbar_wait(k_empty(st), (it / STAGES - 1) & 1, abort_flag, wl);
+                        if (!ok) break;
+                    }
+                    const uint32_t dst = sK + st * L::K_TILE + dst0;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int n0 = t * TM + half * kPageRows;
+                        size_t first = ((size_t)r.b * p.Hkv + r.h) * p.P_max + n0;
+                        if (p.block_table)  // (a page of rows past the end is not read)
+                            first = ((size_t)(n0 < N ? p.block_table[(size_t)r.b * p.max_pages + n0 / kPageRows] : 0) * p.Hkv +
+                                     r.h) * kPageRows;
+                        const uint8_t *src = kc + first * (D * 2) + c16 * 16;
+#pragma unroll
+                        for (int x = 0; x < kPageRows; x += RW) {
+                            const int i = x + r0;
+                            const bool read = n0 + i < N;
+                            copy16(dst + (half * kPageRows + x) * 128, read ? src + (size_t)i * (D * 2) : kc, read);
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;\n" ::: "memory");
+                    if (it - landed >= STAGES - 1) {
+                        asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
+                        tc::fence_proxy_async_smem();
+                        announce(it - (STAGES - 2) + 1);
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");  // (nothing may land after the CTA exits)
+        tc::fence_proxy_async_smem();
+        if (ok) announce(it);
+    } else {
+        // ================= MMA issue =================
+        const bool one = lane == 0;
+        const uint64_t dk = tc::smem_desc_sw128(sK, 16, 1024), dq = tc::smem_desc_sw128(sbase, 16, 1024);
+        int it = 0, turn = 0, run = 0, used[2] = {0, 0};  // K tiles, turns, runs, tiles of each TMEM buffer
+        bool ok = true;
+        Run r;
+        while (one && ok && walk.next(r)) {
+            if (skipped(r)) continue;
+            const int a = rows[r.b], nturn = turns(a), flip = run++ & 1;
+            for (int c = 0; c < nturn && ok; ++c, ++turn) {
+                const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ);
+                const uint32_t id = tc::idesc_bf16_f32(TM, ceil_div(nq, 32) * 32, 0, 0);
+                ok = tc::mbar_wait(q_full(qb), (turn >> 1) & 1, abort_flag, wl);
+                for (int t = r.t0; t < r.t1 && ok; ++t, ++it) {
+                    const int st = it % STAGES, buf = (t - r.t0 + flip) & 1;
+                    const int nu = buf ? used[1]++ : used[0]++;
+                    if (nu > 0) ok = tc::mbar_wait(d_empty(buf), (nu - 1) & 1, abort_flag, wl);
+                    ok = ok && tc::mbar_wait(k_full(st), (it / STAGES) & 1, abort_flag, wl);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t ka = (uint64_t)(kk >> 2) * ((TM * 128) >> 4) + (kk & 3) * 2;
+                        const uint64_t qa = (uint64_t)(kk >> 2) * ((TQ * 128) >> 4) + (kk & 3) * 2;
+                        tc::mma_ss(tbase + buf * TQ, dk + (uint64_t)st * (L::K_TILE >> 4) + ka,
+                                   dq + (uint64_t)qb * (L::Q_BUF >> 4) + qa, id, kk > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(d_full(buf));
+                    tc::mma_commit(k_empty(st));
+                }
+                if (ok) tc::mma_commit(q_empty(qb));
+            }
+        }
+        if (one) {
+            tc::mma_commit(fin);  // every MMA completes before TMEM is freed
+            tc::mbar_wait_drain(fin, 0, wl);
+        }
+        __syncwarp();
+    }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 12) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tbase, 256);
+    }
+    if (tid == 0 && *abort_flag) atomicOr(p.dev_status, TIDAR_DEV_TIMEOUT);
+}
+
+template <int D>
+cudaError_t launch(const MassParams &p, cudaStream_t s) {
+    const int smem = Smem<D>::alloc(p.B);
+    cudaError_t e = cudaFuncSetAttribute(mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kNumSMs, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mass_kernel<D>, p);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t mass_launch(const MassParams &p, cudaStream_t s) {
-    const dim3 grid(32, p.B, p.L * p.Hkv);
-    mass_rows_kernel<<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
 }
 
 }  // namespace tidar
