@@ -3,15 +3,16 @@
 //
 // The products are taken as S^T = K Q^T: 128 keys are the rows of a tile (the lanes of TMEM) and up to 128 queries its
 // columns, so that a key's weights are summed by one thread in a fixed order and written by it alone: no atomics, no
-// exchange.  A key tile feeds all its queries from one read of K; more than 128 queries take turns over the CTA's run of
-// key tiles (from L2), the later ones adding to the mass.
+// exchange.  A key tile feeds all its queries from one read of K: up to 128 queries stay in shared memory while a CTA's
+// run of key tiles streams by; more take turns against four key tiles that stay there meanwhile (so that the next turn's
+// queries arrive while this turn's weights are summed: 1.5 us of latency against 2 us of work).
 //
 // Work: the key tiles of all (layer, sequence, KV head) form one line, cut into equal shares of cost, one per CTA (every
 // SM the same work, whatever the lengths).  The pointers of the layers are on the device, so K comes by cp.async into the
 // swizzled layout, not through tensor maps.
 //
 // A CTA (13 warps): warps 0-3 and 4-7 take the sums of every other key tile, warps 8-11 copy (K tiles through a ring of 4
-// to 8, Q through two buffers), warp 12 issues the MMAs into two TMEM buffers.
+// to 8, Q through two buffers), warp 12 issues the MMAs into two TMEM buffers for each half of the summing warps.
 //
 // Bound by the bytes of K up to about 175 queries per key (a tile's 32 KB take an SM's share of HBM as long as 128 x 175
 // exponentials its MUFU), by the exponentials above.
@@ -26,6 +27,7 @@ constexpr int TM = 128;       // keys of a tile
 constexpr int TQ = 128;       // queries of a turn
 constexpr int THREADS = 416;
 constexpr int COPIERS = 128;  // threads of warps 8-11
+constexpr int GROUP = 4;      // key tiles that stay for several turns (at most the ring)
 constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
 constexpr int kBytesCost = 176;                  // cost of a tile that is bound by its bytes, in queries
 constexpr int kSkip = 1 << 30;                   // in rows[b]: a page out of range
@@ -36,10 +38,10 @@ struct Smem {
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int Q_BUF = TQ * D * 2;
     static constexpr int K_OFF = 2 * Q_BUF;
-    static constexpr int LSE_OFF = K_OFF + STAGES * K_TILE;  // float[2][TQ]: -lse in log2 units
-    static constexpr int BAR_OFF = LSE_OFF + 2 * TQ * 4;
-    // k_full[STAGES], k_empty[STAGES], q_full[2], q_empty[2], d_full[2], d_empty[2], fin
-    static constexpr int NBARS = 2 * STAGES + 9;
+    static constexpr int LSE_OFF = K_OFF + STAGES * K_TILE;  // float[4 turns][TQ]: -lse in log2 units
+    static constexpr int BAR_OFF = LSE_OFF + 4 * TQ * 4;
+    // k_full[STAGES], k_empty[STAGES], q_full[2], q_empty[2], d_full[4], d_empty[4], l_full[4], l_empty[4], fin
+    static constexpr int NBARS = 2 * STAGES + 21;
     static constexpr int MISC_OFF = BAR_OFF + (NBARS * 8 + 15) / 16 * 16;
     static constexpr int SEQ_OFF = MISC_OFF + 16;  // long long cum[B + 1], int tiles[B], int rows[B]
     static int alloc(int B) { return SEQ_OFF + (B + 1) * 8 + B * 8 + 1024; }
@@ -135,6 +137,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// Whether the phase has completed, without the wait of a try (which may hold the thread for microseconds).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P1;\n\tmbarrier.test_wait.parity.shared::cta.b64 P1, [%1], %2;\n\tselp.b32 %0, 1, 0, P1;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool read) {  // zeros where it does not read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
@@ -151,8 +163,10 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
     auto q_full = [&](int i) { return bar0 + 8u * (2 * STAGES + i); };
     auto q_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 2 + i); };
     auto d_full = [&](int i) { return bar0 + 8u * (2 * STAGES + 4 + i); };
-    auto d_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 6 + i); };
-    const uint32_t fin = bar0 + 8u * (2 * STAGES + 8);
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 8 + i); };
+    auto l_full = [&](int i) { return bar0 + 8u * (2 * STAGES + 12 + i); };
+    auto l_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 16 + i); };
+    const uint32_t fin = bar0 + 8u * (2 * STAGES + 20);
     float *nlse = reinterpret_cast<float *>(smem + L::LSE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
@@ -168,15 +182,19 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(q_full(i), COPIERS);
-            tc::mbar_init(q_empty(i), 1 + 8);  // the MMAs and the summing warps (which read the LSEs)
+            tc::mbar_init(q_empty(i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             tc::mbar_init(d_full(i), 1);
             tc::mbar_init(d_empty(i), 128);
+            tc::mbar_init(l_full(i), COPIERS);
+            tc::mbar_init(l_empty(i), 8);  // the summing warps
         }
         tc::mbar_init(fin, 1);
         *abort_flag = 0;
         tc::mbar_fence_init();
     }
-    if (warp == 12) tc::tmem_alloc(smem_u32(tmem_slot), 256);
+    if (warp == 12) tc::tmem_alloc(smem_u32(tmem_slot), 512);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // the line; a sequence whose length or row count is out of range has no tiles
     if (warp == 0) {
@@ -240,71 +258,92 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
         __syncthreads();
     }
     auto skipped = [&](const Run &r) { return (rows[r.b] & kSkip) != 0; };
+    // Queries take `turns` of TQ; with more than one, each against a group of key tiles.
     auto turns = [&](int a) { return ceil_div(a * p.G, TQ); };
+    auto group = [&](const Run &r, int nturn) { return nturn == 1 ? r.t1 - r.t0 : GROUP; };
 
     if (warp < 8) {
         // ================= sums: warpgroup w takes every other tile; thread = key =================
         const int w = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
-        const uint32_t d_col = tbase + ((uint32_t)(q4 * 32) << 16) + w * TQ;
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const uint64_t sl2 = pair(p.scale_log2, p.scale_log2);
-        int turn = 0, run = 0, taken = 0;  // turns, runs, this warpgroup's tiles
+        int turn = 0, run = 0, taken = 0;  // turns, runs, this warpgroup's products
         bool ok = true;
         Run r;
         while (ok && walk.next(r)) {
             if (skipped(r)) continue;
-            const int t0 = r.t0 + ((run++ ^ w) & 1);  // (a key stays with its thread through the turns)
-            const int N = p.prefix_len[r.b], a = rows[r.b], nturn = turns(a);
+            const int flip = (run++ ^ w) & 1;
+            const int N = p.prefix_len[r.b], a = rows[r.b], nturn = turns(a), gs = group(r, nturn);
             float *mass = p.masses[r.l] + ((size_t)r.b * p.Hkv + r.h) * p.P_max;
-            for (int c = 0; c < nturn && ok; ++c, ++turn) {
-                const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ), chunks = ceil_div(nq, 32);
-                const float *nl = nlse + qb * TQ;
-                // (also without a tile: the arrival below is for this turn)
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(q_full(qb), (turn >> 1) & 1, abort_flag, wl));
-                for (int t = t0; t < r.t1 && ok; t += 2) {
-                    const int key = t * TM + row;
-                    const bool mine = key < N;
-                    float old = 0.f;
-                    if (mine && (c > 0 || key < N - a)) old = mass[key];
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(d_full(w), taken & 1, abort_flag, wl));
-                    if (!ok) break;  // (TMEM accesses are warp-wide)
-                    tc::fence_after_sync();
-                    ++taken;
-                    // a newest row n sees only itself and what follows: queries of rows j >= n - (N - a)
-                    const int cmin = max(0, (key - (N - a)) * p.G - c * TQ);
-                    const bool cut = t * TM + TM > N - a;
-                    uint64_t sum[4] = {0, 0, 0, 0};
-                    for (int x = 0; x < chunks; ++x) {
-                        uint32_t u[32];
-                        tc::tmem_ld32(d_col + x * 32, u);
-                        uint64_t nl2[16];
+            for (int g0 = r.t0; g0 < r.t1 && ok; g0 += gs) {
+                const int g1 = min(g0 + gs, r.t1);
+                uint64_t sums[GROUP / 2][4];  // of this warpgroup's tiles of the group, over the turns
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const ulonglong2 v = reinterpret_cast<const ulonglong2 *>(nl + x * 32)[j];
-                            nl2[2 * j] = v.x;
-                            nl2[2 * j + 1] = v.y;
-                        }
-                        tc::tmem_wait_ld();
+                for (int j = 0; j < GROUP / 2 * 4; ++j) sums[j / 4][j % 4] = 0;
+                for (int c = 0; c < nturn && ok; ++c, ++turn) {
+                    const int ls = turn & 3, nq = min(TQ, a * p.G - c * TQ), chunks = ceil_div(nq, 32);
+                    const float *nl = nlse + ls * TQ;
+                    // (also without a tile: the arrival below is for this turn)
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(l_full(ls), (turn >> 2) & 1, abort_flag, wl));
+                    auto tile = [&](int t, uint64_t(&sum)[4]) {
+                        const int key = t * TM + row, buf = 2 * w + (taken & 1);
+                        const uint32_t d_col = tbase + lane_off + buf * TQ;
+                        const bool mine = key < N, last = c == nturn - 1;
+                        float old = 0.f;
+                        if (mine && last && key < N - a) old = mass[key];
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(d_full(buf), (taken >> 1) & 1, abort_flag, wl));
+                        if (!ok) return;  // (TMEM accesses are warp-wide)
+                        ++taken;
+                        tc::fence_after_sync();
+                        // a newest row n sees only itself and what follows: queries of rows j >= n - (N - a)
+                        const int cmin = max(0, (key - (N - a)) * p.G - c * TQ);
+                        const bool cut = t * TM + TM > N - a;
+                        for (int x = 0; x < chunks; ++x) {
+                            uint32_t u[32];
+                            tc::tmem_ld32(d_col + x * 32, u);
+                            uint64_t nl2[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float e, f;
-                            unpair(fma2(pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), sl2, nl2[j]), e, f);
-                            e = fast_exp2(e);
-                            f = fast_exp2(f);
-                            if (cut) {  // by select: a masked weight may be anything
-                                e = x * 32 + 2 * j >= cmin ? e : 0.f;
-                                f = x * 32 + 2 * j + 1 >= cmin ? f : 0.f;
+                            for (int j = 0; j < 8; ++j) {
+                                const ulonglong2 v = reinterpret_cast<const ulonglong2 *>(nl + x * 32)[j];
+                                nl2[2 * j] = v.x;
+                                nl2[2 * j + 1] = v.y;
                             }
-                            sum[j & 3] = add2(sum[j & 3], pair(e, f));
+                            tc::tmem_wait_ld();
+                            if (x == chunks - 1) {
+                                tc::fence_before_sync();
+                                tc::mbar_arrive(d_empty(buf));
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float e, f;
+                                unpair(fma2(pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), sl2, nl2[j]), e, f);
+                                e = fast_exp2(e);
+                                f = fast_exp2(f);
+                                if (cut) {  // by select: a masked weight may be anything
+                                    e = x * 32 + 2 * j >= cmin ? e : 0.f;
+                                    f = x * 32 + 2 * j + 1 >= cmin ? f : 0.f;
+                                }
+                                sum[j & 3] = add2(sum[j & 3], pair(e, f));
+                            }
                         }
+                        if (last) {
+                            float e, f;
+                            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e, f);
+                            if (mine) mass[key] = key < N - a ? fmaf(p.decay, old, e + f) : e + f;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) sum[j] = 0;
+                        }
+                    };
+                    if (nturn == 1) {
+                        for (int t = g0 + flip; t < g1 && ok; t += 2) tile(t, sums[0]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < GROUP / 2; ++j)
+                            if (g0 + flip + 2 * j < g1 && ok) tile(g0 + flip + 2 * j, sums[j]);
                     }
-                    tc::fence_before_sync();
-                    tc::mbar_arrive(d_empty(w));
-                    float e, f;
-                    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), e, f);
-                    if (mine) mass[key] = c > 0 ? old + (e + f) : key < N - a ? fmaf(p.decay, old, e + f) : e + f;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(l_empty(ls));
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(q_empty(qb));
             }
         }
         // sequences without new rows: their sums decay
@@ -324,111 +363,143 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
         constexpr int CH = D / 8, RW = COPIERS / CH;  // 16-byte chunks of a row; rows of one sweep (a multiple of 8)
         const int c16 = ct % CH, r0 = ct / CH;
         const uint32_t dst0 = (c16 >> 3) * TM * 128 + r0 * 128 + (((c16 & 7) ^ (r0 & 7)) << 4);
-        int it = 0, turn = 0, landed = 0;  // K tiles issued, turns, K tiles whose landing has been announced
-        // Every K tile is one copy group, the Q of a turn part of its first tile's group: a tile is announced once at most
-        // STAGES - 2 younger groups are under way.
-        int q_of[2] = {-1, -1};  // per Q buffer: the tile whose group holds it
-        auto announce = [&](int upto) {
-            for (; landed < upto; ++landed) {
-                for (int i = 0; i < 2; ++i)
-                    if (q_of[i] == landed) tc::mbar_arrive(q_full(i));
-                tc::mbar_arrive(k_full(landed % STAGES));
+        int it = 0, turn = 0;  // K tiles, turns
+        // Every K tile and every Q is one copy group; it is announced once at most LAG younger ones are under way.
+        constexpr int LAG = STAGES - 2;
+        uint32_t codes = 0;  // the groups under way, youngest in the low four bits: a K stage, or 8 + turn % 4
+        int under_way = 0;
+        uint32_t has_lse = 0;  // bit turn % 4: this thread copies an LSE of the turn
+        auto announce = [&](int keep) {
+            tc::fence_proxy_async_smem();
+            for (; under_way > keep; --under_way) {
+                const int code = codes >> (4 * (under_way - 1)) & 15;
+                if (code >= 8) {  // the LSE that this thread copied
+                    float *x = nlse + (code - 8) * TQ + ct;
+                    *x = has_lse >> (code - 8) & 1 ? -*x * kLog2e : -INFINITY;
+                    tc::mbar_arrive(l_full(code - 8));
+                }
+                tc::mbar_arrive(code < 8 ? k_full(code) : q_full(code & 1));
             }
+        };
+        auto close = [&](int code) {
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+            codes = codes << 4 | code;
+            if (++under_way > LAG) {
+                asm volatile("cp.async.wait_group %0;\n" ::"n"(LAG) : "memory");
+                announce(LAG);
+            }
+        };
+        // a place that is not free yet may wait for what is under way
+        auto wait_free = [&](uint32_t bar, uint32_t ph) {
+            while (!mbar_test(bar, ph)) {
+                if (under_way == 0) return tc::mbar_wait(bar, ph, abort_flag, wl);
+                switch (under_way - 1) {  // the oldest of them
+                    case 0: asm volatile("cp.async.wait_group 0;\n" ::: "memory"); break;
+                    case 1: asm volatile("cp.async.wait_group 1;\n" ::: "memory"); break;
+                    case 2: asm volatile("cp.async.wait_group 2;\n" ::: "memory"); break;
+                    case 3: asm volatile("cp.async.wait_group 3;\n" ::: "memory"); break;
+                    case 4: asm volatile("cp.async.wait_group 4;\n" ::: "memory"); break;
+                    default: asm volatile("cp.async.wait_group 5;\n" ::: "memory"); break;
+                }
+                announce(under_way - 1);
+            }
+            return true;
         };
         bool ok = true;
         Run r;
         while (ok && walk.next(r)) {
             if (skipped(r)) continue;
-            const int N = p.prefix_len[r.b], a = rows[r.b], nturn = turns(a);
+            const int N = p.prefix_len[r.b], a = rows[r.b], nturn = turns(a), gs = group(r, nturn);
             const uint8_t *kc = static_cast<const uint8_t *>(p.k_caches[r.l]);
             const uint8_t *q = static_cast<const uint8_t *>(p.qs[r.l]) + ((size_t)r.b * p.R * p.Hq + r.h * p.G) * D * 2;
             const float *lse = p.lses[r.l] + (size_t)r.b * p.R * p.Hq + r.h * p.G;
-            for (int c = 0; c < nturn && ok; ++c, ++turn) {
-                const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ);
-                // (the buffer's last reader may still wait for tiles that are on their way: announce them first)
-                if (turn >= 2) {
-                    asm volatile("cp.async.wait_all;\n" ::: "memory");
-                    tc::fence_proxy_async_smem();
-                    announce(it);
-                    ok = tc::mbar_wait(q_empty(qb), ((turn >> 1) - 1) & 1, abort_flag, wl);
+            for (int g0 = r.t0; g0 < r.t1 && ok; g0 += gs) {
+                const int g1 = min(g0 + gs, r.t1);
+                for (int c = 0; c < nturn && ok; ++c, ++turn) {
+                    const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ);
+                    const int ls = turn & 3;
+                    if (turn >= 2) ok = wait_free(q_empty(qb), ((turn >> 1) - 1) & 1);
+                    if (ok && turn >= 4) ok = wait_free(l_empty(ls), ((turn >> 2) - 1) & 1);
                     if (!ok) break;
-                }
-                for (int x = r0; x < (nq + 31) / 32 * 32; x += RW) {
-                    const int i = c * TQ + x, j = i / p.G, gq = i - j * p.G;
-                    copy16(sbase + qb * L::Q_BUF + dst0 + (x - r0) * 128,
-                           q + ((size_t)j * p.Hq + gq) * (x < nq ? D * 2 : 0) + c16 * 16, x < nq);
-                }
-                {
-                    const int i = c * TQ + ct, j = i / p.G, gq = i - j * p.G;
-                    nlse[qb * TQ + ct] = ct < nq ? -lse[(size_t)j * p.Hq + gq] * kLog2e : -INFINITY;
-                }
-                q_of[qb] = it;
-                for (int t = r.t0; t < r.t1; ++t, ++it) {
-                    const int st = it % STAGES;
-                    if (it >= STAGES) {
-                        ok = tc::mbar_wait(k_empty(st), (it / STAGES - 1) & 1, abort_flag, wl);
+                    for (int x = r0; x < (nq + 31) / 32 * 32; x += RW) {
+                        const int i = c * TQ + x, j = i / p.G, gq = i - j * p.G;
+                        copy16(sbase + qb * L::Q_BUF + dst0 + (x - r0) * 128,
+                               q + ((size_t)j * p.Hq + gq) * (x < nq ? D * 2 : 0) + c16 * 16, x < nq);
+                    }
+                    {
+                        const int i = c * TQ + ct, j = i / p.G, gq = i - j * p.G;
+                        if (ct < nq)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(
+                                             sbase + L::LSE_OFF + (ls * TQ + ct) * 4),
+                                         "l"(lse + (size_t)j * p.Hq + gq)
+                                         : "memory");
+                        has_lse = (has_lse & ~(1u << ls)) | (uint32_t)(ct < nq) << ls;
+                    }
+                    close(8 + ls);
+                    if (c > 0) continue;
+                    for (int t = g0; t < g1; ++t, ++it) {
+                        const int st = it % STAGES;
+                        if (it >= STAGES) ok = wait_free(k_empty(st), (it / STAGES - 1) & 1);
                         if (!ok) break;
-                    }
-                    const uint32_t dst = sK + st * L::K_TILE + dst0;
+                        const uint32_t dst = sK + st * L::K_TILE + dst0;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int n0 = t * TM + half * kPageRows;
-                        size_t first = ((size_t)r.b * p.Hkv + r.h) * p.P_max + n0;
-                        if (p.block_table)  // (a page of rows past the end is not read)
-                            first = ((size_t)(n0 < N ? p.block_table[(size_t)r.b * p.max_pages + n0 / kPageRows] : 0) * p.Hkv +
-                                     r.h) * kPageRows;
-                        const uint8_t *src = kc + first * (D * 2) + c16 * 16;
+                        for (int half = 0; half < 2; ++half) {
+                            const int n0 = t * TM + half * kPageRows;
+                            size_t first = ((size_t)r.b * p.Hkv + r.h) * p.P_max + n0;
+                            if (p.block_table)  // (a page of rows past the end is not read)
+                                first = ((size_t)(n0 < N ? p.block_table[(size_t)r.b * p.max_pages + n0 / kPageRows] : 0) *
+                                             p.Hkv + r.h) * kPageRows;
+                            const uint8_t *src = kc + first * (D * 2) + c16 * 16;
 #pragma unroll
-                        for (int x = 0; x < kPageRows; x += RW) {
-                            const int i = x + r0;
-                            const bool read = n0 + i < N;
-                            copy16(dst + (half * kPageRows + x) * 128, read ? src + (size_t)i * (D * 2) : kc, read);
+                            for (int x = 0; x < kPageRows; x += RW) {
+                                const int i = x + r0;
+                                const bool read = n0 + i < N;
+                                copy16(dst + (half * kPageRows + x) * 128, read ? src + (size_t)i * (D * 2) : kc, read);
+                            }
                         }
-                    }
-                    asm volatile("cp.async.commit_group;\n" ::: "memory");
-                    if (it - landed >= STAGES - 1) {
-                        asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
-                        tc::fence_proxy_async_smem();
-                        announce(it - (STAGES - 2) + 1);
+                        close(st);
                     }
                 }
             }
         }
         asm volatile("cp.async.wait_all;\n" ::: "memory");  // (nothing may land after the CTA exits)
-        tc::fence_proxy_async_smem();
-        if (ok) announce(it);
+        if (ok) announce(0);
     } else {
         // ================= MMA issue =================
         const bool one = lane == 0;
         const uint64_t dk = tc::smem_desc_sw128(sK, 16, 1024), dq = tc::smem_desc_sw128(sbase, 16, 1024);
-        int it = 0, turn = 0, run = 0, used[2] = {0, 0};  // K tiles, turns, runs, tiles of each TMEM buffer
+        int it = 0, turn = 0, run = 0, used[2] = {0, 0};  // K tiles, turns, runs, products of each summing half
         bool ok = true;
         Run r;
         while (one && ok && walk.next(r)) {
             if (skipped(r)) continue;
-            const int a = rows[r.b], nturn = turns(a), flip = run++ & 1;
-            for (int c = 0; c < nturn && ok; ++c, ++turn) {
-                const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ);
-                const uint32_t id = tc::idesc_bf16_f32(TM, ceil_div(nq, 32) * 32, 0, 0);
-                ok = tc::mbar_wait(q_full(qb), (turn >> 1) & 1, abort_flag, wl);
-                for (int t = r.t0; t < r.t1 && ok; ++t, ++it) {
-                    const int st = it % STAGES, buf = (t - r.t0 + flip) & 1;
-                    const int nu = buf ? used[1]++ : used[0]++;
-                    if (nu > 0) ok = tc::mbar_wait(d_empty(buf), (nu - 1) & 1, abort_flag, wl);
-                    ok = ok && tc::mbar_wait(k_full(st), (it / STAGES) & 1, abort_flag, wl);
-                    if (!ok) break;
-                    tc::fence_after_sync();
+            const int a = rows[r.b], nturn = turns(a), gs = group(r, nturn), flip = run++ & 1;
+            for (int g0 = r.t0; g0 < r.t1 && ok; g0 += gs) {
+                const int g1 = min(g0 + gs, r.t1);
+                for (int c = 0; c < nturn && ok; ++c, ++turn) {
+                    const int qb = turn & 1, nq = min(TQ, a * p.G - c * TQ);
+                    const uint32_t id = tc::idesc_bf16_f32(TM, ceil_div(nq, 32) * 32, 0, 0);
+                    ok = tc::mbar_wait(q_full(qb), (turn >> 1) & 1, abort_flag, wl);
+                    for (int t = g0; t < g1 && ok; ++t) {
+                        const int i = it + t - g0, st = i % STAGES, w = (t - g0 + flip) & 1;
+                        const int nu = w ? used[1]++ : used[0]++, buf = 2 * w + (nu & 1);
+                        if (nu >= 2) ok = tc::mbar_wait(d_empty(buf), ((nu >> 1) - 1) & 1, abort_flag, wl);
+                        if (ok && c == 0) ok = tc::mbar_wait(k_full(st), (i / STAGES) & 1, abort_flag, wl);
+                        if (!ok) break;
+                        tc::fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t ka = (uint64_t)(kk >> 2) * ((TM * 128) >> 4) + (kk & 3) * 2;
-                        const uint64_t qa = (uint64_t)(kk >> 2) * ((TQ * 128) >> 4) + (kk & 3) * 2;
-                        tc::mma_ss(tbase + buf * TQ, dk + (uint64_t)st * (L::K_TILE >> 4) + ka,
-                                   dq + (uint64_t)qb * (L::Q_BUF >> 4) + qa, id, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t ka = (uint64_t)(kk >> 2) * ((TM * 128) >> 4) + (kk & 3) * 2;
+                            const uint64_t qa = (uint64_t)(kk >> 2) * ((TQ * 128) >> 4) + (kk & 3) * 2;
+                            tc::mma_ss(tbase + buf * TQ, dk + (uint64_t)st * (L::K_TILE >> 4) + ka,
+                                       dq + (uint64_t)qb * (L::Q_BUF >> 4) + qa, id, kk > 0 ? 1u : 0u);
+                        }
+                        tc::mma_commit(d_full(buf));
+                        if (c == nturn - 1) tc::mma_commit(k_empty(st));
                     }
-                    tc::mma_commit(d_full(buf));
-                    tc::mma_commit(k_empty(st));
+                    if (ok) tc::mma_commit(q_empty(qb));
                 }
-                if (ok) tc::mma_commit(q_empty(qb));
+                it += g1 - g0;
             }
         }
         if (one) {
@@ -442,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
     __syncthreads();
     if (warp == 12) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tbase, 256);
+        tc::tmem_dealloc(tbase, 512);
     }
     if (tid == 0 && *abort_flag) atomicOr(p.dev_status, TIDAR_DEV_TIMEOUT);
 }
