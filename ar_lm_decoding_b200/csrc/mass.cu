@@ -147,6 +147,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool read) {  // zeros where it does not read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
@@ -450,11 +453,17 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
                                 first = ((size_t)(n0 < N ? p.block_table[(size_t)r.b * p.max_pages + n0 / kPageRows] : 0) *
                                              p.Hkv + r.h) * kPageRows;
                             const uint8_t *src = kc + first * (D * 2) + c16 * 16;
+                            const uint8_t *at = src + r0 * (D * 2);
+                            if (n0 + kPageRows <= N) {  // (constant offsets: one instruction a copy)
 #pragma unroll
-                            for (int x = 0; x < kPageRows; x += RW) {
-                                const int i = x + r0;
-                                const bool read = n0 + i < N;
-                                copy16(dst + (half * kPageRows + x) * 128, read ? src + (size_t)i * (D * 2) : kc, read);
+                                for (int x = 0; x < kPageRows; x += RW)
+                                    copy16(dst + (half * kPageRows + x) * 128, at + x * (D * 2));
+                            } else {
+#pragma unroll 1
+                                for (int x = 0; x < kPageRows; x += RW) {
+                                    const bool read = n0 + x + r0 < N;
+                                    copy16(dst + (half * kPageRows + x) * 128, read ? at + x * (D * 2) : kc, read);
+                                }
                             }
                         }
                         close(st);
