@@ -424,10 +424,15 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
                     if (turn >= 2) ok = wait_free(q_empty(qb), ((turn >> 1) - 1) & 1);
                     if (ok && turn >= 4) ok = wait_free(l_empty(ls), ((turn >> 2) - 1) & 1);
                     if (!ok) break;
-                    for (int x = r0; x < (nq + 31) / 32 * 32; x += RW) {
-                        const int i = c * TQ + x, j = i / p.G, gq = i - j * p.G;
-                        copy16(sbase + qb * L::Q_BUF + dst0 + (x - r0) * 128,
-                               q + ((size_t)j * p.Hq + gq) * (x < nq ? D * 2 : 0) + c16 * 16, x < nq);
+                    {  // query c TQ + x is row j, head gq
+                        int j = (c * TQ + r0) / p.G, gq = c * TQ + r0 - j * p.G;
+                        const uint8_t *at = q + ((size_t)j * p.Hq + gq) * (D * 2) + c16 * 16;
+                        const uint32_t dst = sbase + qb * L::Q_BUF + dst0 - r0 * 128;
+                        for (int x = r0; x < (nq + 31) / 32 * 32; x += RW) {
+                            copy16(dst + x * 128, x < nq ? at : q, x < nq);
+                            at += RW * D * 2;
+                            for (gq += RW; gq >= p.G; gq -= p.G) at += (size_t)(p.Hq - p.G) * (D * 2);
+                        }
                     }
                     {
                         const int i = c * TQ + ct, j = i / p.G, gq = i - j * p.G;
