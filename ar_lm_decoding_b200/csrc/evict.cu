@@ -3,15 +3,16 @@
 // A cluster of C CTAs takes one (layer, sequence, KV head).  Every CTA finds the rows to give up by itself (the masses
 // are read from L2), then moves its share of the columns of K and V; CTA 0 also moves the masses.
 //
-// Selection: the keepth-greatest mass among the candidates, by histograms over a shrinking range of keys (a monotone
-// 32-bit image of the float).  The first pass takes the exact range of the keys, so its 2048 bins are spread over the
-// values that occur; a range of 2^32 needs at most three passes, ties of equal masses none beyond.  Ties at the
-// threshold go to the lower rows.
+// Selection: the last row to stay, by a histogram of the masses' monotone 32-bit images over their upper 11 bits; the
+// rows of the bin that holds it (256 at most) are ranked against each other by (mass, row), a fuller bin is divided by
+// another histogram, and equal masses by a count over the rows in order.
 //
 // Moves: rows that survive behind the final heavy zone fill the holes inside it pairwise (sources all behind the zone,
-// destinations all inside: no order among the copies).  Then the newest rows slide down by N - budget, tile by tile in
-// ascending order: a tile is loaded before any of it is stored, and a later tile's sources lie behind an earlier
-// tile's destinations.
+// destinations all inside: no order among the copies).  Then the newest rows slide down by N - budget, in ascending
+// order.  Both are one list, taken in tiles: a tile is loaded before any of it is stored, a later tile's sources lie
+// behind an earlier tile's destinations, and a slide's destination is loaded, if it survives, by an earlier item.
+//
+// Bound by the moves' bytes for a long cut, by latency for a step's trim (a few rows of holes and the newest rows).
 #include "cache_ops.cuh"
 #include "tc.cuh"
 
@@ -23,13 +24,20 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int MAXC = 8;
+constexpr int RANKED = 256;         // rows ranked against each other at most
+constexpr int kKeysBytes = 65536;   // images held in shared memory at most (two CTAs of an SM hold as much)
 static_assert(BINS == 4 * THREADS, "four bins a thread in the bin search");
 
 struct EvictSmem {
-    uint32_t hist[BINS];
+    union {
+        uint32_t hist[BINS];
+        uint2 ranked[RANKED];  // (image, row)
+    };
     uint32_t warp_sum[WARPS];
-    uint32_t lo, hi;        // key range under search
-    uint32_t bin, above;    // the bin that holds the keepth-greatest key, keys above it
+    uint32_t bin, above;  // the bin that holds the last row to stay, rows above it
+    uint32_t count;
+    uint32_t T;           // the last row to stay: its image,
+    int row;              // its place
 };
 
 __device__ __forceinline__ uint32_t key_of(float m) {
@@ -69,12 +77,16 @@ __device__ __forceinline__ size_t row_bytes(const EvictParams &p, int b, int kvh
     return row * p.D * 2;
 }
 
-__global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, int C) {
-    extern __shared__ uint16_t lists[];  // holes (from the sink), then the survivors behind the zone (from its end)
+__global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, int C, int cap) {
+    extern __shared__ uint32_t dyn[];  // lists of 16-bit rows (holes from the sink, survivors from the zone's end), images
     __shared__ EvictSmem sm;
     const int tid = threadIdx.x, part = blockIdx.x % C, head = blockIdx.x / C;
     const int kvh = head % p.Hkv, b = head / p.Hkv % p.B, l = head / p.Hkv / p.B;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // (evict_lengths_kernel waits for this grid's end)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm.hist[i * THREADS + tid] = 0;
+    if (tid == 0) sm.count = 0;
     const int N = p.prefix_len[b];
     const bool bad = N < 0 || N > p.P_max;
     if (bad || N <= p.budget) {  // (uniform over the cluster)
@@ -85,44 +97,27 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
         if (tid == 0) atomicOr(p.dev_status, TIDAR_DEV_BAD_PAGE);
         return;
     }
+    __syncthreads();
     float *mass = p.masses[l] + ((size_t)b * p.Hkv + kvh) * p.P_max;
-    const int zone = p.budget - p.recent;      // [sink, zone): the heaviest rows
-    const int lo = p.sink, hi = N - p.recent;  // candidates
-    const int keep = zone - p.sink;            // of them stay
+    const int zone = p.budget - p.recent;            // [sink, zone): the heaviest rows
+    const int lo = p.sink, n = N - p.recent - lo;    // candidates: rows lo .. lo + n - 1
+    const int keep = zone - p.sink;                  // of them stay
+    uint16_t *lists = reinterpret_cast<uint16_t *>(dyn);
+    uint32_t *keys = dyn + cap;
+    const bool held = n * 4 <= kKeysBytes;
+    auto key = [&](int i) { return held ? keys[i] : key_of(mass[lo + i]); };
 
-    // ---- the keepth-greatest key T; of the keys equal to T the first need_eq rows stay ----
-    uint32_t T = 0xffffffffu, need_eq = 0;
-    bool ties = false;
+    // ---- the last candidate to stay: image T, place `last` among the candidates ----
+    uint32_t T = 0xffffffffu;
+    int last = -1;
     if (keep > 0) {
-        uint32_t kmin = 0xffffffffu, kmax = 0;
-        for (int i = lo + tid; i < hi; i += THREADS) {
-            const uint32_t k = key_of(mass[i]);
-            kmin = min(kmin, k);
-            kmax = max(kmax, k);
+        for (int i = tid; i < n; i += THREADS) {
+            const uint32_t k = key_of(mass[lo + i]);
+            if (held) keys[i] = k;
+            atomicAdd(&sm.hist[k >> 21], 1u);
         }
-        kmin = __reduce_min_sync(0xffffffffu, kmin);
-        kmax = __reduce_max_sync(0xffffffffu, kmax);
-        if (tid == 0) {
-            sm.lo = 0xffffffffu;
-            sm.hi = 0;
-        }
-        __syncthreads();
-        if ((tid & 31) == 0) {
-            atomicMin(&sm.lo, kmin);
-            atomicMax(&sm.hi, kmax);
-        }
-        __syncthreads();
-        uint32_t rlo = sm.lo, rhi = sm.hi, want = keep, equal = hi - lo;
-        while (rlo < rhi) {  // (each pass divides the range by up to 2048: at most three)
-            const int bits = 32 - __clz(rhi - rlo);
-            const int shift = max(0, bits - 11);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sm.hist[i * THREADS + tid] = 0;
-            __syncthreads();
-            for (int i = lo + tid; i < hi; i += THREADS) {
-                const uint32_t k = key_of(mass[i]);
-                if (k >= rlo && k <= rhi) atomicAdd(&sm.hist[(k - rlo) >> shift], 1u);
-            }
+        uint32_t base = 0, want = keep;  // images from base on, of which the want-th greatest is sought
+        for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
             __syncthreads();
             // bins from the top: thread t has bins 2047 - 4t .. 2044 - 4t
             uint32_t c[4], mine = 0, all;
@@ -143,100 +138,124 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
                 }
             }
             __syncthreads();
-            const uint32_t bin = sm.bin;
+            const uint32_t inside = sm.hist[sm.bin], span = (1u << shift) - 1u;
+            base += sm.bin << shift;
             want -= sm.above;
-            equal = sm.hist[bin];
-            rlo += bin << shift;
-            rhi = rlo + min(rhi - rlo, (1u << shift) - 1u);
             __syncthreads();
+            if (inside <= RANKED) {
+                for (int i = tid; i < n; i += THREADS) {
+                    const uint32_t k = key(i);
+                    if (k >= base && k - base <= span) sm.ranked[atomicAdd(&sm.count, 1u)] = make_uint2(k, i);
+                }
+                __syncthreads();
+                if (tid < (int)inside) {
+                    const uint2 me = sm.ranked[tid];
+                    uint32_t first = 0;
+                    for (int i = 0; i < (int)inside; ++i) {
+                        const uint2 o = sm.ranked[i];
+                        first += o.x > me.x || (o.x == me.x && o.y < me.y);
+                    }
+                    if (first == want - 1) {
+                        sm.T = me.x;
+                        sm.row = (int)me.y;
+                    }
+                }
+                __syncthreads();
+                T = sm.T;
+                last = sm.row;
+                break;
+            }
+            if (shift == 0) {  // more equal images than can be ranked: the want-th of them in the order of the rows
+                const int per = ceil_div(n, THREADS), i0 = min(n, tid * per), i1 = min(n, i0 + per);
+                uint32_t eq = 0, all_eq;
+                for (int i = i0; i < i1; ++i) eq += key(i) == base;
+                uint32_t seen = block_scan(eq, sm.warp_sum, &all_eq);
+                if (seen < want && want <= seen + eq) {
+                    for (int i = i0; i < i1; ++i)
+                        if (key(i) == base && ++seen == want) sm.row = i;
+                }
+                __syncthreads();
+                T = base;
+                last = sm.row;
+                break;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sm.hist[i * THREADS + tid] = 0;
+            __syncthreads();
+            const int sub = shift == 21 ? 10 : 0;
+            for (int i = tid; i < n; i += THREADS) {
+                const uint32_t k = key(i);
+                if (k >= base && k - base <= span) atomicAdd(&sm.hist[(k - base) >> sub], 1u);
+            }
         }
-        T = rlo;
-        need_eq = want;
-        ties = want < equal;
+    } else if (held) {
+        for (int i = tid; i < n; i += THREADS) keys[i] = 0;
+        __syncthreads();
     }
 
     // ---- holes and the survivors that fill them: a contiguous run of candidates per thread, in row order ----
-    const int per = ceil_div(hi - lo, THREADS);
-    const int i0 = min(hi, lo + tid * per), i1 = min(hi, i0 + per);
-    uint32_t eq_before = 0;
-    if (ties) {
-        uint32_t eq = 0, all;
-        for (int i = i0; i < i1; ++i) eq += key_of(mass[i]) == T;
-        eq_before = block_scan(eq, sm.warp_sum, &all);
-    }
-    auto stays = [&](int i, uint32_t &eq) {
-        const uint32_t k = key_of(mass[i]);
-        bool s = keep > 0 && k >= T;
-        if (k == T && ties) s = keep > 0 && eq++ < need_eq;
-        return s;
+    const int per = ceil_div(n, THREADS), i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    auto stays = [&](int i) {
+        const uint32_t k = key(i);
+        return keep > 0 && (k > T || (k == T && i <= last));
     };
-    uint32_t count = 0, eq = eq_before, total;  // holes in the upper half word, survivors in the lower
+    uint32_t count = 0, total;  // holes in the upper half word, survivors in the lower
     for (int i = i0; i < i1; ++i) {
-        const bool s = stays(i, eq);
-        if (i < zone && !s) count += 1u << 16;
-        if (i >= zone && s) count += 1;
+        const bool s = stays(i);
+        if (i < keep && !s) count += 1u << 16;
+        if (i >= keep && s) count += 1;
     }
-    const uint32_t base = block_scan(count, sm.warp_sum, &total);
+    const uint32_t before = block_scan(count, sm.warp_sum, &total);
     const int moves = total & 0xffffu;
     uint16_t *holes = lists, *tails = lists + moves;
-    uint32_t h = base >> 16, t = base & 0xffffu;
-    eq = eq_before;
-    for (int i = i0; i < i1; ++i) {
-        const bool s = stays(i, eq);
-        if (i < zone && !s) holes[h++] = (uint16_t)(i - p.sink);
-        if (i >= zone && s) tails[t++] = (uint16_t)(i - zone);
+    uint32_t h = before >> 16, t = before & 0xffffu;
+    if (count) {
+        for (int i = i0; i < i1; ++i) {
+            const bool s = stays(i);
+            if (i < keep && !s) holes[h++] = (uint16_t)i;
+            if (i >= keep && s) tails[t++] = (uint16_t)(i - keep);
+        }
     }
     __syncthreads();
     if (C > 1) tc::cluster_sync();  // every CTA has read the masses
+
+    // ---- the list of moves: item i < moves fills a hole, the others slide ----
+    const int rows = moves + p.recent;
+    auto source = [&](int i) { return i < moves ? zone + tails[i] : N - p.recent + (i - moves); };
+    auto target = [&](int i) { return i < moves ? p.sink + holes[i] : zone + (i - moves); };
     if (part == 0) {
-        for (int i = tid; i < moves; i += THREADS) mass[p.sink + holes[i]] = mass[zone + tails[i]];
-        for (int i = 0; i < p.recent; i += THREADS) {
-            const float m = i + tid < p.recent ? mass[N - p.recent + i + tid] : 0.f;
-            __syncthreads();  // (before the first tile is stored the survivors behind the zone have left it, too)
-            if (i + tid < p.recent) mass[zone + i + tid] = m;
+        for (int i = 0; i < rows; i += THREADS) {
+            const float m = i + tid < rows ? mass[source(i + tid)] : 0.f;
+            __syncthreads();
+            if (i + tid < rows) mass[target(i + tid)] = m;
         }
     }
-
-    // ---- this CTA's columns of K and V: vectors [v0, v0 + vn) of a row of D/8, of K (x = 0) or V (x = 1) ----
-    const int vec = p.D / 8;
-    const int x0 = C == 1 ? 0 : part & 1, x1 = C == 1 ? 2 : x0 + 1;
+    // This CTA's columns of K and V: vectors [v0, v0 + vn) of a row of D/8, of K (x = 0) and V (x = 1) or of one of them.
+    const int vec = p.D / 8, nx = C == 1 ? 2 : 1;
     const int vn = C <= 2 ? vec : vec / (C / 2), v0 = C <= 2 ? 0 : (part >> 1) * vn;
-    for (int x = x0; x < x1; ++x) {
-        uint8_t *cache = static_cast<uint8_t *>(x ? p.v_caches[l] : p.k_caches[l]);
-        constexpr int U = 4;
-        for (int i = tid; i < moves * vn; i += U * THREADS) {
-            uint4 v[U];
+    uint8_t *cache[2] = {static_cast<uint8_t *>(C > 1 && (part & 1) ? p.v_caches[l] : p.k_caches[l]),
+                         static_cast<uint8_t *>(p.v_caches[l])};
+    const int per_row = vn * nx, bits = 31 - __clz(per_row);  // (powers of two)
+    constexpr int U = 8;
+    for (int i0 = 0; i0 < rows * per_row; i0 += U * THREADS) {
+        uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = i + u * THREADS;
-                if (it < moves * vn)
-                    v[u] = *reinterpret_cast<const uint4 *>(cache + row_bytes(p, b, kvh, zone + tails[it / vn]) +
-                                                            (v0 + it % vn) * 16);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = i + u * THREADS;
-                if (it < moves * vn)
-                    *reinterpret_cast<uint4 *>(cache + row_bytes(p, b, kvh, p.sink + holes[it / vn]) +
-                                               (v0 + it % vn) * 16) = v[u];
+        for (int u = 0; u < U; ++u) {
+            const int it = i0 + u * THREADS + tid;
+            if (it < rows * per_row) {
+                const int c = it & (per_row - 1);
+                v[u] = *reinterpret_cast<const uint4 *>(cache[c >= vn] + row_bytes(p, b, kvh, source(it >> bits)) +
+                                                        (v0 + (c & (vn - 1))) * 16);
             }
         }
         __syncthreads();
-        for (int i0 = 0; i0 < p.recent * vn; i0 += U * THREADS) {
-            uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = i0 + u * THREADS + tid;
-                if (it < p.recent * vn)
-                    v[u] = *reinterpret_cast<const uint4 *>(cache + row_bytes(p, b, kvh, N - p.recent + it / vn) +
-                                                            (v0 + it % vn) * 16);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = i0 + u * THREADS + tid;
-                if (it < p.recent * vn)
-                    *reinterpret_cast<uint4 *>(cache + row_bytes(p, b, kvh, zone + it / vn) + (v0 + it % vn) * 16) = v[u];
+        for (int u = 0; u < U; ++u) {
+            const int it = i0 + u * THREADS + tid;
+            if (it < rows * per_row) {
+                const int c = it & (per_row - 1);
+                *reinterpret_cast<uint4 *>(cache[c >= vn] + row_bytes(p, b, kvh, target(it >> bits)) +
+                                           (v0 + (c & (vn - 1))) * 16) = v[u];
             }
         }
     }
@@ -261,7 +280,7 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     // Few heads: a cluster per head, so that the moves use more SMs (and more loads in flight).
     int C = 1;
     while (C < MAXC && heads * C * 2 <= 2 * kNumSMs) C *= 2;
-    const int smem = 2 * 2 * cap;
+    const int smem = 4 * cap + min(4 * max(0, p.P_max - p.recent - p.sink), kKeysBytes);
     cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -278,7 +297,7 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, evict_kernel, p, C);
+    e = cudaLaunchKernelEx(&cfg, evict_kernel, p, C, cap);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.B, 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
