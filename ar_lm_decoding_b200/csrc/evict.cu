@@ -38,6 +38,7 @@ struct EvictSmem {
     uint32_t count;
     uint32_t T;           // the last row to stay: its image,
     int row;              // its place
+    int pages[kMaxPagesPerSeq];  // of the sequence (paged caches)
 };
 
 __device__ __forceinline__ uint32_t key_of(float m) {
@@ -69,14 +70,6 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sum, u
     return before + x - v;
 }
 
-// Byte offset of cache row n of (b, kvh).
-__device__ __forceinline__ size_t row_bytes(const EvictParams &p, int b, int kvh, int n) {
-    size_t row = ((size_t)b * p.Hkv + kvh) * p.P_max + n;
-    if (p.block_table)
-        row = ((size_t)p.block_table[(size_t)b * p.max_pages + n / kPageRows] * p.Hkv + kvh) * kPageRows + n % kPageRows;
-    return row * p.D * 2;
-}
-
 __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, int C, int cap) {
     extern __shared__ uint32_t dyn[];  // lists of 16-bit rows (holes from the sink, survivors from the zone's end), images
     __shared__ EvictSmem sm;
@@ -93,9 +86,17 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
         if (bad && tid == 0) atomicOr(p.dev_status, TIDAR_DEV_BAD_PREFIX);
         return;
     }
-    if (p.block_table && block_bad_page(p.block_table + (size_t)b * p.max_pages, N, p.num_pages)) {
-        if (tid == 0) atomicOr(p.dev_status, TIDAR_DEV_BAD_PAGE);
-        return;
+    if (p.block_table) {
+        bool bad_page = false;
+        for (int i = tid; i < ceil_div(N, kPageRows); i += THREADS) {
+            const int pg = p.block_table[(size_t)b * p.max_pages + i];
+            bad_page |= pg < 0 || pg >= p.num_pages;
+            sm.pages[i] = pg;
+        }
+        if (__syncthreads_or(bad_page)) {
+            if (tid == 0) atomicOr(p.dev_status, TIDAR_DEV_BAD_PAGE);
+            return;
+        }
     }
     __syncthreads();
     float *mass = p.masses[l] + ((size_t)b * p.Hkv + kvh) * p.P_max;
@@ -111,10 +112,18 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
     uint32_t T = 0xffffffffu;
     int last = -1;
     if (keep > 0) {
-        for (int i = tid; i < n; i += THREADS) {
-            const uint32_t k = key_of(mass[lo + i]);
-            if (held) keys[i] = k;
-            atomicAdd(&sm.hist[k >> 21], 1u);
+        constexpr int U = 8;  // loads under way
+        for (int i0 = tid; i0 < n; i0 += U * THREADS) {
+            float m[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) m[u] = i0 + u * THREADS < n ? mass[lo + i0 + u * THREADS] : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u * THREADS >= n) break;
+                const uint32_t k = key_of(m[u]);
+                if (held) keys[i0 + u * THREADS] = k;
+                atomicAdd(&sm.hist[k >> 21], 1u);
+            }
         }
         uint32_t base = 0, want = keep;  // images from base on, of which the want-th greatest is sought
         for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
@@ -235,6 +244,11 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
     const int vn = C <= 2 ? vec : vec / (C / 2), v0 = C <= 2 ? 0 : (part >> 1) * vn;
     uint8_t *cache[2] = {static_cast<uint8_t *>(C > 1 && (part & 1) ? p.v_caches[l] : p.k_caches[l]),
                          static_cast<uint8_t *>(p.v_caches[l])};
+    const size_t first = ((size_t)b * p.Hkv + kvh) * p.P_max;
+    auto row_bytes = [&](int i) {  // byte offset of cache row i
+        const size_t row = p.block_table ? ((size_t)sm.pages[i / kPageRows] * p.Hkv + kvh) * kPageRows + i % kPageRows : first + i;
+        return row * (p.D * 2);
+    };
     const int per_row = vn * nx, bits = 31 - __clz(per_row);  // (powers of two)
     constexpr int U = 8;
     for (int i0 = 0; i0 < rows * per_row; i0 += U * THREADS) {
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
             const int it = i0 + u * THREADS + tid;
             if (it < rows * per_row) {
                 const int c = it & (per_row - 1);
-                v[u] = *reinterpret_cast<const uint4 *>(cache[c >= vn] + row_bytes(p, b, kvh, source(it >> bits)) +
+                v[u] = *reinterpret_cast<const uint4 *>(cache[c >= vn] + row_bytes(source(it >> bits)) +
                                                         (v0 + (c & (vn - 1))) * 16);
             }
         }
@@ -254,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
             const int it = i0 + u * THREADS + tid;
             if (it < rows * per_row) {
                 const int c = it & (per_row - 1);
-                *reinterpret_cast<uint4 *>(cache[c >= vn] + row_bytes(p, b, kvh, target(it >> bits)) +
+                *reinterpret_cast<uint4 *>(cache[c >= vn] + row_bytes(target(it >> bits)) +
                                            (v0 + (c & (vn - 1))) * 16) = v[u];
             }
         }
