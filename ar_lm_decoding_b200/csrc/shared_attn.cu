@@ -38,8 +38,10 @@ constexpr int TH = 64;  // keys of half a tile
 constexpr int THREADS = 384;
 constexpr int BOXR = kPageRows;
 // Cost of one key tile for a block of two row tiles and of one, and of a block's start and end (Q, the record), where
-// every CTA has a few tiles (see Line): measured ~3,900, ~2,700 and ~3,000 cycles.
-constexpr int kCostPair = 3, kCostSingle = 2, kCostBlock = 2;
+// every CTA has a few tiles (see Line): measured ~3,300, ~2,900 and ~4,200 cycles, the ratio then tuned on the whole call
+// (8 x Qwen3-8B k 8: 66.3 us with 3 : 2 : 2, 60.5 with 8 : 7 : 10, 60.6 with 8 : 6 : 12; 16 single-token rows: 23.4, 23.0,
+// 22.3 us).
+constexpr int kCostPair = 8, kCostSingle = 6, kCostBlock = 12;
 constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
 
 // The line of key tiles (cum[b], beside it: key tiles of the sequences before b, nseq[b]: sequences before b that have
@@ -237,7 +239,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// The greater of three; NaN if one of them is.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// The greatest of three; NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float d;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -831,19 +843,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::tmem_wait_ld();
                 float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < D; ++j) a4[j & 3] = fmaxf(a4[j & 3], fabsf(__uint_as_float(v[j >> 5][j & 31])));
+                for (int j = 0; j < D; j += 2)
+                    a4[(j >> 1) & 3] = max3(a4[(j >> 1) & 3], fabsf(__uint_as_float(v[j >> 5][j & 31])),
+                                            fabsf(__uint_as_float(v[j >> 5][(j + 1) & 31])));
                 const float amax = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
                 const float rs = amax > 0.f ? __fdividef(1.f, amax) : 0.f;
                 if (valid) {
                     uint8_t *rec = p.ws + info + ((size_t)(cta + sg.id) * 2 + t) * tile_record_bytes(D);
                     uint4 *vals = reinterpret_cast<uint4 *>(rec) + row;
+                    const uint64_t rs2 = pair(rs, rs);
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
-                        float f[8];
+                        uint32_t h[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[c >> 2][(c & 3) * 8 + e]) * rs;
-                        vals[c * TM] = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]),
-                                                  pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = (c & 3) * 8 + 2 * e;
+                            float x, y;
+                            unpair(mul2(pair(__uint_as_float(v[c >> 2][j]), __uint_as_float(v[c >> 2][j + 1])), rs2), x, y);
+                            h[e] = pack_half2(x, y);
+                        }
+                        vals[c * TM] = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                     reinterpret_cast<float2 *>(rec + TM * D * 2)[row] =
                         make_float2(l_run == 0.f ? -INFINITY : m_run + __log2f(l_run),  // (a NaN sum stays one)
