@@ -182,12 +182,12 @@ struct Smem {
     static constexpr int SEG_OFF = (BAR_OFF + NBARS * 8 + 63) / 64 * 64;
     static constexpr int LINE_OFF = SEG_OFF + SEGS * (int)sizeof(Segment);
     static constexpr int MISC_OFF = LINE_OFF + 64;
-    static constexpr int CUM_OFF = MISC_OFF + 16;  // int[B + 1] twice
-    static int alloc(int B) { return CUM_OFF + 2 * (B + 1) * 4 + 1024; }
+    static constexpr int CUM_OFF = MISC_OFF + 16;  // int[B + 1] three times
+    static int alloc(int B) { return CUM_OFF + 3 * (B + 1) * 4 + 1024; }
 };
 static_assert(sizeof(Line) <= 64, "the line's place in shared memory");
-static_assert(Smem<128>::CUM_OFF + 2 * (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024 &&
-                  Smem<64>::CUM_OFF + 2 * (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024,
+static_assert(Smem<128>::CUM_OFF + 3 * (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024 &&
+                  Smem<64>::CUM_OFF + 3 * (kMaxBatchShared + 1) * 4 + 1024 <= 227 * 1024,
               "shared memory beyond 227 KB");
 
 // One lane of the (converged) warp, the same one every time.
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     Line *line = reinterpret_cast<Line *>(smem + L::LINE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
-    int *cum = reinterpret_cast<int *>(smem + L::CUM_OFF), *nseq = cum + p.B + 1;
+    int *cum = reinterpret_cast<int *>(smem + L::CUM_OFF), *nseq = cum + p.B + 1, *lens = nseq + p.B + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Geometry g = geometry(p.B, p.R, p.G);
 
@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int x = 0;
             if (b < p.B) {
                 const int P = p.prefix_len[b];
+                lens[b] = P;
                 if (P >= 0 && P <= p.P_max) x = ceil_div(P, TN) + ceil_div(p.R, TN);
             }
             int inc = x;
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (; more; ++n) {
                 if (n >= SEGS && !tc::mbar_wait(seg_empty(n % SEGS), (n / SEGS - 1) & 1, abort_flag, wl)) break;
                 more = walk.next(sg);
-                sg.len = !more ? 0 : sg.b < 0 ? S : p.prefix_len[sg.b];
+                sg.len = !more ? 0 : sg.b < 0 ? S : lens[sg.b];
                 segs[n % SEGS] = sg;
                 tc::mbar_arrive(seg_full(n % SEGS));
                 if (!more) break;
