@@ -1,6 +1,8 @@
 // Parameters of the shared-prefix attention, the attention mass and the cache eviction.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace tidar {
@@ -59,6 +61,20 @@ struct EvictParams {
 };
 
 cudaError_t evict_launch(const EvictParams &p, cudaStream_t s);
+
+// Lets kernel K take `bytes` of dynamic shared memory, once per device (the call costs a launch's tenth).
+template <auto K>
+cudaError_t allow_shared_memory(int bytes) {
+    static std::atomic<unsigned long long> done{0};  // bit = device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Whether one of the pages holding rows [0, n) of a table row is outside [0, num_pages); every thread of the block
 // calls it and gets the answer.

@@ -295,7 +295,7 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     int C = 1;
     while (C < MAXC && heads * C * 2 <= 2 * kNumSMs) C *= 2;
     const int smem = 4 * cap + min(4 * max(0, p.P_max - p.recent - p.sink), kKeysBytes);
-    cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_shared_memory<evict_kernel>(kMaxEvictRows / 2 * 4 + kKeysBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(heads * C, 1, 1);

@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
 template <int D>
 cudaError_t launch(const MassParams &p, cudaStream_t s) {
     const int smem = Smem<D>::alloc(p.B);
-    cudaError_t e = cudaFuncSetAttribute(mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_shared_memory<mass_kernel<D>>(Smem<D>::alloc(kMaxBatchShared));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kNumSMs, 1, 1);

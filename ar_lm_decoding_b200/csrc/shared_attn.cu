@@ -1050,16 +1050,21 @@ cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
     const long long s_rows = no_shared ? 1 : (long long)p.Hkv * p.S_max;
     const long long o_rows = no_own ? 1 : (long long)p.B * p.Hkv * p.P_max;
     const int box = paged ? BOXR : TN;
-    if (!map_2d(&mp.ks, paged || !no_shared ? p.k_shared : p.q, D, paged ? pool_rows : s_rows, box) ||
-        !map_2d(&mp.vs, paged || !no_shared ? p.v_shared : p.q, D, paged ? pool_rows : s_rows, box) ||
-        !map_2d(&mp.kc, paged || !no_own ? p.k_cache : p.q, D, paged ? pool_rows : o_rows, box) ||
+    if (!paged && (!map_2d(&mp.ks, no_shared ? p.q : p.k_shared, D, s_rows, box) ||
+                   !map_2d(&mp.vs, no_shared ? p.q : p.v_shared, D, s_rows, box)))
+        return cudaErrorInvalidValue;
+    if (!map_2d(&mp.kc, paged || !no_own ? p.k_cache : p.q, D, paged ? pool_rows : o_rows, box) ||
         !map_2d(&mp.vc, paged || !no_own ? p.v_cache : p.q, D, paged ? pool_rows : o_rows, box) ||
         !map_3d(&mp.kn, p.k_new, D, p.Hkv, (long long)p.B * p.R, 1, TN) ||
         !map_3d(&mp.vn, p.v_new, D, p.Hkv, (long long)p.B * p.R, 1, TN) ||
         !map_3d(&mp.q, p.q, D, p.Hq, (long long)p.B * p.R, p.G, rows_per_tile(p.G)))
         return cudaErrorInvalidValue;
+    if (paged) {  // (the shared rows lie in the same pools)
+        mp.ks = mp.kc;
+        mp.vs = mp.vc;
+    }
     const int smem = Smem<D>::alloc(p.B);
-    cudaError_t e = cudaFuncSetAttribute(shared_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_shared_memory<shared_attn_kernel<D>>(Smem<D>::alloc(kMaxBatchShared));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kNumSMs, 1, 1);
