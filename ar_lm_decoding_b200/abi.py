@@ -52,6 +52,10 @@ _SIGS = {
     "tidar_verify_commit": (_i, [_vp, _vp, _i] + [_vp] * 4 + [_f] + [_vp] * 5 + [_i] * 9 + [_vp] * 12
                             + [_vp, _sz, _vp, _vp]),
     "tidar_testing_attn_step_stalled": (_i, [_vp] * 6 + [_i] * 6 + [_f, _i] + [_vp, _vp, _vp, ctypes.c_longlong, _vp]),
+    "tidar_testing_attn_step_shared_stalled": (_i, [_vp] * 6 + [_i] + [_vp] * 3 + [_i] * 7 + [_f, _i] + [_vp] * 3
+                                               + [_sz, _vp, ctypes.c_longlong, _vp]),
+    "tidar_testing_attn_mass_stalled": (_i, [_vp] * 5 + [_i, _i, _vp, _vp] + [_i] * 7
+                                        + [_f, _f, _vp, ctypes.c_longlong, _vp]),
     "tidar_testing_attn_splits": (_i, [_i] * 6),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -176,6 +180,26 @@ def tidar_testing_attn_step_stalled(q, k_new, v_new, k_cache, v_cache, prefix_le
     _check("tidar_testing_attn_step_stalled", _lib.tidar_testing_attn_step_stalled(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_len), B, Hq, Hkv, D, k, P_max,
         softmax_scale, mask_mode, _ptr(out), _ptr(lse), _ptr(dev_status), wait_cycles, _stream(stream)))
+
+
+def tidar_testing_attn_step_shared_stalled(q, k_new, v_new, k_shared, v_shared, shared_len, S_max, k_cache, v_cache,
+                                           prefix_len, B, Hq, Hkv, D, k, R, P_max, softmax_scale, mask_mode, out, lse,
+                                           workspace, ws_bytes, dev_status, wait_cycles, stream=None) -> None:
+    """Test hook (include/tidar_testing.h): the shared-prefix attention with a wait that runs out on purpose."""
+    _check("tidar_testing_attn_step_shared_stalled", _lib.tidar_testing_attn_step_shared_stalled(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_shared), _ptr(v_shared), _ptr(shared_len), S_max, _ptr(k_cache),
+        _ptr(v_cache), _ptr(prefix_len), B, Hq, Hkv, D, k, R, P_max, softmax_scale, mask_mode, _ptr(out), _ptr(lse),
+        _ptr(workspace), ws_bytes, _ptr(dev_status), wait_cycles, _stream(stream)))
+
+
+def tidar_testing_attn_mass_stalled(qs, lses, k_caches, masses, block_table, max_pages, num_pages, prefix_len,
+                                    row_count, L, B, Hq, Hkv, D, R, P_max, softmax_scale, decay, dev_status,
+                                    wait_cycles, stream=None) -> None:
+    """Test hook (include/tidar_testing.h): the attention mass with a wait that runs out on purpose."""
+    _check("tidar_testing_attn_mass_stalled", _lib.tidar_testing_attn_mass_stalled(
+        _ptr(qs), _ptr(lses), _ptr(k_caches), _ptr(masses), _ptr(block_table), max_pages, num_pages,
+        _ptr(prefix_len), _ptr(row_count), L, B, Hq, Hkv, D, R, P_max, softmax_scale, decay, _ptr(dev_status),
+        wait_cycles, _stream(stream)))
 
 
 def tidar_testing_attn_splits(B, Hq, Hkv, D, k, P_max) -> int:

@@ -292,14 +292,15 @@ namespace {
 // Sizes of the shared-prefix attention that do not depend on the layout of the caches.
 tidar_status check_shared(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max) {
     if (B < 1 || Hq < 1 || Hkv < 1 || R < 1 || S_max < 0 || P_max < 0) return TIDAR_ERR_INVALID_ARG;
-    if (Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128) || B > kMaxBatchShared || R > kMaxCausalRows)
+    if (Hq % Hkv != 0 || Hq / Hkv > 128 || Hkv > 65535 || (D != 64 && D != 128) || B > kMaxBatchShared || R > kMaxCausalRows)
         return TIDAR_ERR_UNSUPPORTED;
     if ((long long)B * R * Hq >= (1LL << 31)) return TIDAR_ERR_UNSUPPORTED;
     if (!shared_attn_fits(B, R, Hkv, Hq / Hkv, S_max, P_max)) return TIDAR_ERR_UNSUPPORTED;
     return TIDAR_OK;
 }
 
-tidar_status attn_shared(SharedAttnParams p, int S_max, int P_max, size_t ws_bytes, float softmax_scale, void *stream) {
+tidar_status attn_shared(SharedAttnParams p, int S_max, int P_max, size_t ws_bytes, float softmax_scale, void *stream,
+                         long long wait_cycles = kCacheWaitCycles, int stall_test = 0) {
     if (!p.q || !p.k_new || !p.v_new || !p.shared_len || !p.prefix_len || !p.out || !p.dev_status)
         return TIDAR_ERR_INVALID_ARG;
     if (!aligned16(p.q) || !aligned16(p.k_new) || !aligned16(p.v_new) || !aligned16(p.k_shared) ||
@@ -323,6 +324,8 @@ tidar_status attn_shared(SharedAttnParams p, int S_max, int P_max, size_t ws_byt
     p.S_max = S_max;
     p.P_max = P_max;
     p.scale_log2 = softmax_scale * kLog2e;
+    p.wait_cycles = wait_cycles;
+    p.stall_test = stall_test;
     return launched(shared_attn_launch(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -333,11 +336,11 @@ size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, in
     return shared_attn_workspace_bytes(B, Hq, Hkv, D, R, S_max, P_max);
 }
 
-tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void *v_new, const void *k_shared,
+static tidar_status attn_shared_contiguous(const void *q, const void *k_new, const void *v_new, const void *k_shared,
                                     const void *v_shared, const int32_t *shared_len, int S_max, const void *k_cache,
                                     const void *v_cache, const int32_t *prefix_len, int B, int Hq, int Hkv, int D,
                                     int k, int R, int P_max, float softmax_scale, int mask_mode, void *out, float *lse,
-                                    void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream) {
+                                    void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream, long long wait_cycles, int stall_test) {
     const tidar_status st = check_shared(B, Hq, Hkv, D, R, S_max, P_max);
     if (st != TIDAR_OK) return st;
     if ((long long)Hkv * S_max >= (1LL << 31) || (long long)B * Hkv * P_max >= (1LL << 31))
@@ -365,7 +368,27 @@ tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void
     p.lse = lse;
     p.ws = static_cast<uint8_t *>(workspace);
     p.dev_status = dev_status;
-    return attn_shared(p, S_max, P_max, ws_bytes, softmax_scale, stream);
+    return attn_shared(p, S_max, P_max, ws_bytes, softmax_scale, stream, wait_cycles, stall_test);
+}
+
+tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void *v_new, const void *k_shared,
+                                    const void *v_shared, const int32_t *shared_len, int S_max, const void *k_cache,
+                                    const void *v_cache, const int32_t *prefix_len, int B, int Hq, int Hkv, int D,
+                                    int k, int R, int P_max, float softmax_scale, int mask_mode, void *out, float *lse,
+                                    void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream) {
+    return attn_shared_contiguous(q, k_new, v_new, k_shared, v_shared, shared_len, S_max, k_cache, v_cache, prefix_len, B, Hq, Hkv, D, k, R,
+                                  P_max, softmax_scale, mask_mode, out, lse, workspace, ws_bytes, dev_status, stream, kCacheWaitCycles,
+                                  0);
+}
+
+tidar_status tidar_testing_attn_step_shared_stalled(const void *q, const void *k_new, const void *v_new, const void *k_shared,
+                                    const void *v_shared, const int32_t *shared_len, int S_max, const void *k_cache,
+                                    const void *v_cache, const int32_t *prefix_len, int B, int Hq, int Hkv, int D,
+                                    int k, int R, int P_max, float softmax_scale, int mask_mode, void *out, float *lse,
+                                    void *workspace, size_t ws_bytes, int32_t *dev_status, long long wait_cycles, void *stream) {
+    if (wait_cycles < 1) return TIDAR_ERR_INVALID_ARG;
+    return attn_shared_contiguous(q, k_new, v_new, k_shared, v_shared, shared_len, S_max, k_cache, v_cache, prefix_len, B, Hq, Hkv, D, k, R,
+                                  P_max, softmax_scale, mask_mode, out, lse, workspace, ws_bytes, dev_status, stream, wait_cycles, 1);
 }
 
 tidar_status tidar_attn_step_shared_paged(const void *q, const void *k_new, const void *v_new, const void *k_pool,
@@ -408,11 +431,11 @@ tidar_status tidar_attn_step_shared_paged(const void *q, const void *k_new, cons
     return attn_shared(p, S_max, P_max, ws_bytes, softmax_scale, stream);
 }
 
-tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, const void *const *k_caches,
+static tidar_status attn_mass(const void *const *qs, const float *const *lses, const void *const *k_caches,
                              float *const *masses, const int32_t *block_table, int max_pages, int num_pages,
                              const int32_t *prefix_len, const int32_t *row_count, int L, int B, int Hq, int Hkv,
                              int D, int R, int P_max, float softmax_scale, float decay, int32_t *dev_status,
-                             void *stream) {
+                             void *stream, long long wait_cycles, int stall_test) {
     if (L < 1 || B < 1 || Hq < 1 || Hkv < 1 || R < 1) return TIDAR_ERR_INVALID_ARG;
     if (Hq % Hkv != 0 || (D != 64 && D != 128) || B > kMaxBatchShared) return TIDAR_ERR_UNSUPPORTED;
     if (block_table) {
@@ -422,15 +445,33 @@ tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, co
     } else if (P_max < 0) {
         return TIDAR_ERR_INVALID_ARG;
     }
-    if (P_max > kMaxMassRows || (long long)R * Hq >= (1LL << 31) || (long long)L * Hkv >= (1LL << 16) / 2)
-        return TIDAR_ERR_UNSUPPORTED;
+    if (P_max > kMaxMassRows || (long long)R * Hq >= (1LL << 31)) return TIDAR_ERR_UNSUPPORTED;
     if (!qs || !lses || !k_caches || !masses || !prefix_len || !dev_status) return TIDAR_ERR_INVALID_ARG;
     if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return TIDAR_ERR_INVALID_ARG;
     if (!std::isfinite(decay) || !(decay >= 0.f)) return TIDAR_ERR_INVALID_ARG;
     MassParams p{qs, lses, k_caches, masses, block_table, block_table ? max_pages : 0, block_table ? num_pages : 0,
                  prefix_len, row_count, L, B, Hq, Hkv, D, R, Hq / Hkv, P_max, softmax_scale * kLog2e, decay,
-                 dev_status};
+                 dev_status, wait_cycles, stall_test};
     return launched(mass_launch(p, static_cast<cudaStream_t>(stream)));
+}
+
+tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, const void *const *k_caches,
+                             float *const *masses, const int32_t *block_table, int max_pages, int num_pages,
+                             const int32_t *prefix_len, const int32_t *row_count, int L, int B, int Hq, int Hkv,
+                             int D, int R, int P_max, float softmax_scale, float decay, int32_t *dev_status,
+                             void *stream) {
+    return attn_mass(qs, lses, k_caches, masses, block_table, max_pages, num_pages, prefix_len, row_count, L, B, Hq, Hkv, D, R,
+                     P_max, softmax_scale, decay, dev_status, stream, kCacheWaitCycles, 0);
+}
+
+tidar_status tidar_testing_attn_mass_stalled(const void *const *qs, const float *const *lses, const void *const *k_caches,
+                             float *const *masses, const int32_t *block_table, int max_pages, int num_pages,
+                             const int32_t *prefix_len, const int32_t *row_count, int L, int B, int Hq, int Hkv,
+                             int D, int R, int P_max, float softmax_scale, float decay, int32_t *dev_status,
+                             long long wait_cycles, void *stream) {
+    if (wait_cycles < 1) return TIDAR_ERR_INVALID_ARG;
+    return attn_mass(qs, lses, k_caches, masses, block_table, max_pages, num_pages, prefix_len, row_count, L, B, Hq, Hkv, D, R,
+                     P_max, softmax_scale, decay, dev_status, stream, wait_cycles, 1);
 }
 
 tidar_status tidar_kv_evict(void *const *k_caches, void *const *v_caches, float *const *masses,

@@ -7,6 +7,7 @@
 
 namespace tidar {
 
+constexpr long long kCacheWaitCycles = 4000000000LL;  // bound of the on-chip waits of a normal launch (about 2 s)
 constexpr int kMaxBatchShared = 1024;     // longest batch the shared-prefix attention and the mass accept
 constexpr int kMaxSharedPages = 4096;     // longest shared page table (262144 shared tokens)
 constexpr int kMaxCausalRows = 4096;      // most rows per sequence of the causal shared-prefix attention
@@ -27,6 +28,8 @@ struct SharedAttnParams {
     float *lse;  // [B, R, Hq] or null
     uint8_t *ws;
     int32_t *dev_status;
+    long long wait_cycles;  // bound of every on-chip wait, in SM clock cycles
+    int stall_test;         // 1: the MMA issuers first wait on a barrier nothing arrives on (timeout test)
 };
 
 // Whether the cost of the call's key tiles counts in 32 bits.
@@ -45,6 +48,8 @@ struct MassParams {
     int L, B, Hq, Hkv, D, R, G, P_max;
     float scale_log2, decay;
     int32_t *dev_status;
+    long long wait_cycles;  // as in SharedAttnParams
+    int stall_test;
 };
 
 cudaError_t mass_launch(const MassParams &p, cudaStream_t s);

@@ -28,7 +28,6 @@ constexpr int TQ = 128;       // queries of a turn
 constexpr int THREADS = 416;
 constexpr int COPIERS = 128;  // threads of warps 8-11
 constexpr int GROUP = 4;      // key tiles that stay for several turns (at most the ring)
-constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
 constexpr int kBytesCost = 176;                  // cost of a tile that is bound by its bytes, in queries
 constexpr int kSkip = 1 << 30;                   // in rows[b]: a page out of range
 
@@ -40,8 +39,8 @@ struct Smem {
     static constexpr int K_OFF = 2 * Q_BUF;
     static constexpr int LSE_OFF = K_OFF + STAGES * K_TILE;  // float[4 turns][TQ]: -lse in log2 units
     static constexpr int BAR_OFF = LSE_OFF + 4 * TQ * 4;
-    // k_full[STAGES], k_empty[STAGES], q_full[2], q_empty[2], d_full[4], d_empty[4], l_full[4], l_empty[4], fin
-    static constexpr int NBARS = 2 * STAGES + 21;
+    // k_full[STAGES], k_empty[STAGES], q_full[2], q_empty[2], d_full[4], d_empty[4], l_full[4], l_empty[4], fin, stall
+    static constexpr int NBARS = 2 * STAGES + 22;
     static constexpr int MISC_OFF = BAR_OFF + (NBARS * 8 + 15) / 16 * 16;
     static constexpr int SEQ_OFF = MISC_OFF + 16;  // long long cum[B + 1], int tiles[B], int rows[B]
     static int alloc(int B) { return SEQ_OFF + (B + 1) * 8 + B * 8 + 1024; }
@@ -169,14 +168,14 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
     auto d_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 8 + i); };
     auto l_full = [&](int i) { return bar0 + 8u * (2 * STAGES + 12 + i); };
     auto l_empty = [&](int i) { return bar0 + 8u * (2 * STAGES + 16 + i); };
-    const uint32_t fin = bar0 + 8u * (2 * STAGES + 20);
+    const uint32_t fin = bar0 + 8u * (2 * STAGES + 20), stall = fin + 8u;  // (nothing arrives on stall: timeout test)
     float *nlse = reinterpret_cast<float *>(smem + L::LSE_OFF);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF + 4);
     long long *cum = reinterpret_cast<long long *>(smem + L::SEQ_OFF);
     int *tiles = reinterpret_cast<int *>(cum + p.B + 1), *rows = tiles + p.B;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long wl = kWaitCycles;
+    const long long wl = p.wait_cycles;
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -194,6 +193,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
             tc::mbar_init(l_empty(i), 8);  // the summing warps
         }
         tc::mbar_init(fin, 1);
+        tc::mbar_init(stall, 1);
         *abort_flag = 0;
         tc::mbar_fence_init();
     }
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
         const bool one = lane == 0;
         const uint64_t dk = tc::smem_desc_sw128(sK, 16, 1024), dq = tc::smem_desc_sw128(sbase, 16, 1024);
         int it = 0, turn = 0, run = 0, used[2] = {0, 0};  // K tiles, turns, runs, products of each summing half
-        bool ok = true;
+        bool ok = !one || !p.stall_test || tc::mbar_wait(stall, 0, abort_flag, wl);
         Run r;
         while (one && ok && walk.next(r)) {
             if (skipped(r)) continue;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
         }
         if (one) {
             tc::mma_commit(fin);  // every MMA completes before TMEM is freed
-            tc::mbar_wait_drain(fin, 0, wl);
+            tc::mbar_wait_drain(fin, 0, kCacheWaitCycles);
         }
         __syncwarp();
     }

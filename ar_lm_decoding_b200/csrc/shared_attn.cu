@@ -42,7 +42,6 @@ constexpr int BOXR = kPageRows;
 // (8 x Qwen3-8B k 8: 66.3 us with 3 : 2 : 2, 60.5 with 8 : 7 : 10, 60.6 with 8 : 6 : 12; 16 single-token rows: 23.4, 23.0,
 // 22.3 us).
 constexpr int kCostPair = 8, kCostSingle = 6, kCostBlock = 12;
-constexpr long long kWaitCycles = 4000000000LL;  // bound of every on-chip wait (about 2 s)
 
 // The line of key tiles (cum[b], beside it: key tiles of the sequences before b, nseq[b]: sequences before b that have
 // any).  Every CTA's share is at least the cost of one tile, so the CTAs from a block's first tile to its last all have
@@ -177,8 +176,8 @@ struct Smem {
     static constexpr int KV_OFF = 2 * Q_TILE;
     static constexpr int BAR_OFF = KV_OFF + STAGES * KV_TILE;
     // full[STAGES], empty[STAGES], q_full, q_empty, per row tile and S buffer s_full, p_full, pv_done, per row tile
-    // o_full, o_free, per MMA issuer fin; seg_full[SEGS], seg_empty[SEGS]
-    static constexpr int NBARS = 2 * STAGES + 2 + 12 + 8 + 2 * SEGS;
+    // o_full, o_free, fin; stall, seg_full[SEGS], seg_empty[SEGS]
+    static constexpr int NBARS = 2 * STAGES + 2 + 12 + 6 + 2 + 2 * SEGS;
     static constexpr int SEG_OFF = (BAR_OFF + NBARS * 8 + 63) / 64 * 64;
     static constexpr int LINE_OFF = SEG_OFF + SEGS * (int)sizeof(Segment);
     static constexpr int MISC_OFF = LINE_OFF + 64;
@@ -325,7 +324,7 @@ __device__ __noinline__ RowState raise_max(uint32_t sc, int k0, int lo, int glo,
     const float f = grow && m > -INFINITY ? fast_exp2(m - mx) : 1.f;
     if (__any_sync(0xffffffffu, f < 1.f)) {
         // O is at rest once the last half's PV has completed: the next one awaits this half's P
-        st.ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_bar, pv_phase, abort_flag, kWaitCycles));
+        st.ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_bar, pv_phase, abort_flag, kCacheWaitCycles));
         if (!st.ok) return st;
         tc::fence_after_sync();
         st.l *= f;
@@ -369,6 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto o_full = [&](int t) { return q_full + 112u + 8u * t; };
     auto o_free = [&](int t) { return q_full + 128u + 8u * t; };
     auto fin = [&](int i) { return q_full + 144u + 8u * i; };
+    const uint32_t stall = q_full + 160u;  // nothing arrives here (timeout test)
     auto seg_full = [&](int i) { return q_full + 176u + 8u * i; };
     auto seg_empty = [&](int i) { return q_full + 176u + 8u * (SEGS + i); };
     Segment *segs = reinterpret_cast<Segment *>(smem + L::SEG_OFF);
@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mbar_init(o_free(t), 128);
         }
         for (int i = 0; i < 2; ++i) tc::mbar_init(fin(i), 1);
+        tc::mbar_init(stall, 1);
         for (int i = 0; i < SEGS; ++i) {
             tc::mbar_init(seg_full(i), 1);
             tc::mbar_init(seg_empty(i), kSegReaders);
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tbase = *tmem_slot;
     const int cta = blockIdx.x;
     const size_t info = info_bytes((size_t)p.Hkv * g.blocks, p.B);
-    const long long wl = kWaitCycles;
+    const long long wl = p.wait_cycles;
 
     // The next segment for the calling thread (`all`: for its whole warp, which calls it together).
     int seg_at = 0;
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tc::tma_load_3d(sbase + t * L::Q_TILE + h * TM * 128, &maps.q, h * 64, sg.kvh * p.G, z, q_full);
                 }
             }
-            if (n > 0) tc::mbar_wait_drain(q_full, (n - 1) & 1, wl);
+            if (n > 0) tc::mbar_wait_drain(q_full, (n - 1) & 1, kCacheWaitCycles);
         } else if (warp == 0 && lane == 0) {
             // ================= K/V producer =================
             int it = 0;
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // nothing may land after the CTA exits: only the last copy of each stage can still be in flight
             for (int i = max(0, it - STAGES); i < it; ++i)
-                tc::mbar_wait_drain(full(i % STAGES), (i / STAGES) & 1, wl);
+                tc::mbar_wait_drain(full(i % STAGES), (i / STAGES) & 1, kCacheWaitCycles);
         } else if (warp & 1) {
             // ================= MMA issue: warp 1 for row tile 0, warp 3 for row tile 1 =================
             // (The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.)
@@ -628,6 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++c.seg;
             };
             auto halves = [&](const Cursor &c) { return c.i == c.one0 || c.i == c.one1 ? 1 : 2; };
+            if (p.stall_test) ok = wait(stall, 0);
             while (ok) {
                 while (busy != 3 && more) {  // S
                     if (!q.in) {
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             commit(fin(t));  // every MMA completes before TMEM is freed
-            if (one) tc::mbar_wait_drain(fin(t), 0, wl);
+            if (one) tc::mbar_wait_drain(fin(t), 0, kCacheWaitCycles);
             __syncwarp();
         }
         __syncwarp();

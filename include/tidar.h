@@ -25,6 +25,8 @@
  * - All pointers are DEVICE pointers unless stated otherwise.  The caller owns
  *   every buffer; the library allocates no device memory, keeps no pointer
  *   after a call returns and holds no per-call state.
+ * - A call launches on the current device, which has to be the stream's and
+ *   the buffers'.
  * - Every call is asynchronous: it validates its scalar arguments on the host,
  *   enqueues its kernels on `stream` (a cudaStream_t; NULL = legacy default
  *   stream) and returns.  Outputs are valid in stream order.
@@ -177,12 +179,16 @@ size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, in
  *             non-finite visible cache row, reaches every row of its sequence
  *             (a shared one, every row of the batch); masked k_new may hold
  *             anything.
- * workspace   >= tidar_attn_shared_workspace_size(...) bytes, 256-byte aligned
+ * workspace   >= tidar_attn_shared_workspace_size(...) bytes, 256-byte aligned; what it
+ *             held does not matter.  Calls that may run at the same time (two
+ *             streams, two replayed graphs) need one each.
  * dev_status  TIDAR_DEV_BAD_PREFIX: a prefix length out of range (that
  *             sequence's rows are not written) or a shared length out of range
  *             (no row is written).
- * Hq/Hkv <= 128, B <= 1024, D in {64, 128}; Hkv * S_max, B * Hkv * P_max and
- * B * R * Hq below 2^31 (else TIDAR_ERR_UNSUPPORTED).
+ * Hq/Hkv <= 128, Hkv < 65536, B <= 1024, D in {64, 128}; Hkv * S_max, B * Hkv *
+ * P_max and B * R * Hq below 2^31, and so few row tiles times key tiles that
+ * their cost (at most 8 a pair of row tiles and 128 keys, 12 a pair) counts in
+ * 31 bits (else TIDAR_ERR_UNSUPPORTED).
  */
 tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void *v_new,
                                     const void *k_shared, const void *v_shared, const int32_t *shared_len,
@@ -507,8 +513,10 @@ tidar_status tidar_verify_commit(const void *p_logits, const void *q_logits, int
  *           NULL: R for every sequence
  * R >= 1 rows per sequence in q and lse; decay finite and >= 0 (1: a plain sum).
  * dev_status   TIDAR_DEV_BAD_PREFIX, TIDAR_DEV_BAD_ACCEPT (row_count) or
- *           TIDAR_DEV_BAD_PAGE: that sequence's masses are left as they were.
- * D in {64, 128}; B <= 1024, P_max <= 2^22, R * Hq < 2^31 and L * Hkv < 2^15 (else TIDAR_ERR_UNSUPPORTED);
+ *           TIDAR_DEV_BAD_PAGE: that sequence's masses are left as they were.  (The
+ *           pages of a sequence without new rows are not looked at: its masses
+ *           only decay.)
+ * D in {64, 128}; B <= 1024, P_max <= 2^22 and R * Hq < 2^31 (else TIDAR_ERR_UNSUPPORTED);
  * q and the caches 16-byte aligned (the pointers are on the device: not checked).
  */
 tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, const void *const *k_caches,
@@ -542,6 +550,8 @@ tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, co
  * k_caches, v_caches  device arrays of L device pointers (bf16 caches or pools)
  * masses              device array of L device pointers, f32 [B, Hkv, P_max]
  * block_table, max_pages, num_pages, P_max  as for tidar_attn_mass
+ *                     (a page belongs to one sequence: the rows of a page in two
+ *                     block-table rows would be moved twice)
  * prefix_len          int32 [B], read and updated in place
  * budget, sink, recent >= 0 with sink + recent <= budget
  * dev_status  TIDAR_DEV_BAD_PREFIX, TIDAR_DEV_BAD_PAGE: that sequence is left

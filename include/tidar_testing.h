@@ -36,6 +36,29 @@ tidar_status tidar_testing_attn_step_stalled(const void *q, const void *k_new, c
                                              int32_t *dev_status, long long wait_cycles, void *stream);
 
 /*
+ * tidar_attn_step_shared with a wait that runs out on purpose: the threads that
+ * issue the MMAs first wait, for wait_cycles (>= 1) SM clock cycles at most, on
+ * a barrier nothing arrives on.  Everything else as in
+ * tidar_testing_attn_step_stalled.
+ */
+tidar_status tidar_testing_attn_step_shared_stalled(const void *q, const void *k_new, const void *v_new,
+                                                    const void *k_shared, const void *v_shared,
+                                                    const int32_t *shared_len, int S_max, const void *k_cache,
+                                                    const void *v_cache, const int32_t *prefix_len, int B, int Hq,
+                                                    int Hkv, int D, int k, int R, int P_max, float softmax_scale,
+                                                    int mask_mode, void *out, float *lse, void *workspace,
+                                                    size_t ws_bytes, int32_t *dev_status, long long wait_cycles,
+                                                    void *stream);
+
+/* tidar_attn_mass with a wait that runs out on purpose (as above). */
+tidar_status tidar_testing_attn_mass_stalled(const void *const *qs, const float *const *lses,
+                                             const void *const *k_caches, float *const *masses,
+                                             const int32_t *block_table, int max_pages, int num_pages,
+                                             const int32_t *prefix_len, const int32_t *row_count, int L, int B,
+                                             int Hq, int Hkv, int D, int R, int P_max, float softmax_scale,
+                                             float decay, int32_t *dev_status, long long wait_cycles, void *stream);
+
+/*
  * The cluster size (key splits per row tile) tidar_attn_step would use for
  * these sizes on the current device (the largest that keeps every row tile's
  * cluster resident in one wave; 1 when even single CTAs need several waves),

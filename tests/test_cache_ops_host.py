@@ -101,7 +101,7 @@ def test_mass_invalid(abi, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(Hq=5), dict(D=256), dict(B=1025), dict(P_max=(1 << 22) + 1), dict(bt=P, mp=1025, npg=9),
-                                dict(R=1 << 30, Hq=4), dict(L=1 << 14)], ids=str)
+                                dict(R=1 << 30, Hq=4)], ids=str)
 def test_mass_unsupported(abi, kw):
     assert _mass(abi, **kw) == UNSUPPORTED
 
@@ -116,3 +116,10 @@ def test_evict_invalid(abi, kw):
 @pytest.mark.parametrize("kw", [dict(D=80), dict(P_max=65537), dict(bt=P, mp=1025, npg=4), dict(L=1 << 20, B=1 << 10)], ids=str)
 def test_evict_unsupported(abi, kw):
     assert _evict(abi, **kw) == UNSUPPORTED
+
+
+def test_stalled_hooks_invalid(abi):
+    assert _status(abi, abi.tidar_testing_attn_step_shared_stalled, P, P, P, P, P, P, 256, P, P, P, 2, 4, 2, 64, 2, 8, 128,
+                   0.125, 0, P, P, P, 1 << 40, ST, 0) == INVALID
+    assert _status(abi, abi.tidar_testing_attn_mass_stalled, P, P, P, P, None, 0, 0, P, P, 2, 2, 4, 2, 64, 8, 128, 0.125,
+                   1.0, ST, 0) == INVALID

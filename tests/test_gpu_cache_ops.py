@@ -124,6 +124,9 @@ SHARED = [  # B, Hq, Hkv, D, k, R, S, lens
     (1, 128, 1, 64, 1, 3, 300, [40]),
     (2, 4, 4, 128, 0, 77, 333, [5, 150]),
     (3, 8, 2, 64, 0, 300, 90, [0, 70, 200]),
+    (1, 2, 1, 128, 0, 1000, 130, [33]),
+    (1000, 2, 1, 64, 0, 1, 140, [i % 3 for i in range(1000)]),
+    (3, 10, 2, 128, 7, 63, 64, [64, 65, 192]),
 ]
 
 
@@ -167,6 +170,59 @@ def test_shared_attention_does_not_depend_on_timing_or_neighbours(abi, paged):
     assert torch.equal(s.out, first) and bool((s.lse == 7.0).all())
     s.call()
     assert torch.equal(s.out, first) and torch.equal(s.lse, lse)
+
+
+def test_shared_attention_without_caches(abi):
+    """No shared rows, no own rows, neither: the parts that are empty need no memory."""
+    for S, n in ((200, 0), (0, 90), (0, 0)):
+        s = Shared(abi, 13, 3, 6, 2, 64, 3, 15, S, [n] * 3, S_extra=0, P_extra=0)
+        abi.tidar_attn_step_shared(
+            s.q, s.kn, s.vn, s.ks if S else None, s.vs if S else None, s.shared_len, S, s.kc if n else None,
+            s.vc if n else None, s.prefix_len, s.B, s.Hq, s.Hkv, s.D, s.k, s.R, n, s.scale, s.mode, s.out, s.lse, s.ws,
+            s.ws.numel(), s.status)
+        assert s.status.item() == 0
+        s.check()
+
+
+def test_shared_attention_two_calls_at_once(abi):
+    """Two graphs with a workspace each, replayed on two streams at the same time, give what each gives alone."""
+    calls = [Shared(abi, 20 + i, 4, 8, 2, 128, 4, 24, 700 + 300 * i, [0, 100, 300, 64], paged=i == 1) for i in (0, 1)]
+    want, graphs = [], []
+    for s in calls:
+        s.call()
+        want.append((s.out.clone(), s.lse.clone()))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                s.call(stream=torch.cuda.current_stream())
+        graphs.append(g)
+        s.out.fill_(NAN)
+        s.lse.fill_(NAN)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, (o, z) in zip(calls, want):
+        assert s.status.item() == 0
+        assert torch.equal(s.out, o) and torch.equal(s.lse, z)
+
+
+def test_shared_attention_wait_that_runs_out(abi):
+    """A wait that expires is reported, and the context and the same buffers stay usable."""
+    s = Shared(abi, 14, 2, 8, 2, 128, 2, 8, 900, [100, 300])
+    s.ws.fill_(0)
+    abi.tidar_testing_attn_step_shared_stalled(
+        s.q, s.kn, s.vn, s.ks, s.vs, s.shared_len, s.S_max, s.kc, s.vc, s.prefix_len, s.B, s.Hq, s.Hkv, s.D, s.k, s.R,
+        s.P_max, s.scale, s.mode, s.out, s.lse, s.ws, s.ws.numel(), s.status, 200000)
+    assert s.status.item() == abi.TIDAR_DEV_TIMEOUT
+    s.status.zero_()
+    s.call()
+    assert s.status.item() == 0
+    s.check()
 
 
 def test_shared_attention_large_scores(abi):
@@ -389,6 +445,44 @@ def test_attention_mass_sums_to_the_visible_share(abi):
     c.add_mass(abi, q, lse, None, 1.0)
     total = c.mass[0][0, :, :n].double().sum(1)
     assert bool(((total - a * 4).abs() <= 2e-4 * a * 4).all())
+
+
+def test_attention_mass_wait_that_runs_out(abi):
+    c = Caches(25, 2, 2, 2, 128, [700, 300])
+    q, lse = _normal(c.g, 2, 2, 8, 4, 128), torch.full((2, 2, 8, 4), 6.0, device=DEV)
+    before = [m.clone() for m in c.mass]
+    k, _, m, _ = c.args(abi)
+    qs, ls = abi.pointer_array(list(q), DEV), abi.pointer_array(list(lse), DEV)
+    abi.tidar_testing_attn_mass_stalled(qs, ls, k, m, None, 0, 0, c.prefix_len, None, 2, 2, 4, 2, 128, 8, c.P_max,
+                                        128**-0.5, 1.0, c.status, 200000)
+    assert c.status.item() == abi.TIDAR_DEV_TIMEOUT
+    c.status.zero_()
+    for x, y in zip(c.mass, before):
+        x.copy_(y)
+    c.add_mass(abi, q, lse, None, 1.0)
+    assert c.status.item() == 0
+    for l in range(2):
+        for b, n in enumerate((700, 300)):
+            want = ref.mass_update(before[l][b], q[l, b], lse[l, b], c.kc[l][b], n, 8, 128**-0.5, 1.0)
+            assert bool(((c.mass[l][b, :, :n].double() - want[:, :n]).abs() <= ref.MASS_RTOL * want[:, :n]).all())
+
+
+def test_attention_mass_same_bits_twice(abi):
+    """The sums do not depend on timing: the same bits from the same start, also on another stream."""
+    c = Caches(26, 3, 4, 2, 64, [900, 77, 0, 512])
+    q, lse = _normal(c.g, 3, 4, 40, 12, 64), torch.full((3, 4, 40, 12), 6.5, device=DEV)
+    before, got = [m.clone() for m in c.mass], []
+    side = torch.cuda.Stream()
+    for stream in (None, None, side):
+        for x, y in zip(c.mass, before):
+            x.copy_(y)
+        side.wait_stream(torch.cuda.current_stream())
+        c.add_mass(abi, q, lse, _i32([40, 30, 0, 7]), 0.75, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        got.append([m.clone() for m in c.mass])
+    assert c.status.item() == 0
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
 
 
 def test_attention_mass_bad_inputs(abi):
