@@ -41,11 +41,15 @@ constexpr int BOXR = kPageRows;
 // every CTA has a few tiles (see Line): measured ~3,300, ~2,900 and ~4,200 cycles, the ratio then tuned on the whole call
 // (8 x Qwen3-8B k 8: 66.3 us with 3 : 2 : 2, 60.5 with 8 : 7 : 10, 60.6 with 8 : 6 : 12; 16 single-token rows: 23.4, 23.0,
 // 22.3 us).
+constexpr int kLongBlock = 6;  // key tiles from which a block of a short line has two tiles a CTA
 constexpr int kCostPair = 8, kCostSingle = 6, kCostBlock = 12;
 
 // The line of key tiles (cum[b], beside it: key tiles of the sequences before b, nseq[b]: sequences before b that have
 // any).  Every CTA's share is at least the cost of one tile, so the CTAs from a block's first tile to its last all have
-// a part of it: where there are too few tiles for that every tile costs 1 and as many CTAs work as there are tiles.
+// a part of it: where there are too few tiles for that every tile costs 1 and as many CTAs work as there are tiles, or
+// half as many where a block has many of them, so that its rows have fewer records to join (8 x Qwen2.5-1.5B k 4 over 8
+// shared and up to 9 own tiles: 21.7 us with a CTA per tile, 19.6 with one per two; 2 x the tiny shape, 1 and 2 tiles: 9.0
+// and 11.4).
 struct Line {
     int total;               // cost of all KV heads
     int head;                // cost of one KV head
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int S = p.shared_len[0];
     if (S < 0 || S > p.S_max) S = 0;  // (combine_kernel reports it and writes nothing)
     if (warp == 3) {  // the line: key tiles of every sequence (none where the length is out of range)
-        int sum = 0, seqs = 0;
+        int sum = 0, seqs = 0, longest = ceil_div(S, TN);
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             int x = 0;
@@ -439,6 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             sum += __shfl_sync(0xffffffffu, inc, 31);
             seqs += __popc(any);
+            longest = max(longest, (int)__reduce_max_sync(0xffffffffu, (unsigned)x));
         }
         if (lane == 0) {
             cum[p.B] = sum;
@@ -455,8 +460,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 l.total = l.head * p.Hkv;
             };
             lay(kCostPair, kCostSingle, kCostBlock);
-            if (l.total < n * (kCostPair + kCostBlock)) lay(1, 1, 0);
-            l.ncta = min(n, l.total);
+            l.ncta = n;
+            if (l.total < n * (kCostPair + kCostBlock)) {
+                lay(1, 1, 0);
+                l.ncta = min(n, longest < kLongBlock ? l.total : (l.total + 1) / 2);
+            }
             *line = l;
         }
     }
@@ -887,14 +895,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins the records of kJoin rows of one KV head; a thread has 16 columns of one row.  A row has as many
-// records as CTAs worked on its two blocks; their headers are read all at once (a group of threads per record), their values four
-// at a time (the first four beside the headers), in the order of the line.  Also reports lengths and pages out of range and
+// records as CTAs worked on its two blocks; their headers are read all at once (a group of threads per record), their values U at
+// a time (the first U beside the headers), in the order of the line: eight where there are fewer blocks than CTAs, so that
+// a block is split over several, four elsewhere, for more threads on an SM (eight everywhere: 22.5 -> 22.1 us for 16
+// single-token rows, but 62.2 -> 65.8 us for 8 x Qwen3-8B k 8).  Also reports lengths and pages out of range and
 // leaves those rows alone.
 constexpr int kHeads = 64;  // records whose headers are held at a time
 constexpr int kJoin = 16;   // rows of a CTA
-template <int D>
+template <int D, int U>
 __global__ void __launch_bounds__(D / 16 * kJoin) combine_kernel(const SharedAttnParams p) {
-    constexpr int GROUPS = D / 16, U = 4;
+    constexpr int GROUPS = D / 16;
     __shared__ float2 heads[kHeads][kJoin];
     const int lane = threadIdx.x % kJoin, chunk = threadIdx.x / kJoin;
     const int kvh = blockIdx.y;
@@ -1083,7 +1093,8 @@ cudaError_t launch(const SharedAttnParams &p, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(((long long)p.B * p.R * p.G + kJoin - 1) / kJoin), p.Hkv, 1);
     cfg.blockDim = dim3(D / 16 * kJoin, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<D>, p);
+    const long long blocks = (long long)p.Hkv * geometry(p.B, p.R, p.G).blocks;
+    e = cudaLaunchKernelEx(&cfg, blocks < kNumSMs ? combine_kernel<D, 8> : combine_kernel<D, 4>, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
