@@ -25,7 +25,7 @@ constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int MAXC = 8;
 constexpr int RANKED = 256;         // rows ranked against each other at most
-constexpr int kKeysBytes = 65536;   // images held in shared memory at most (two CTAs of an SM hold as much)
+constexpr int kSmemBytes = 227 * 1024 - 14 * 1024;  // dynamic shared memory at most (EvictSmem is static)
 static_assert(BINS == 4 * THREADS, "four bins a thread in the bin search");
 
 struct EvictSmem {
@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sum, u
     return before + x - v;
 }
 
-__global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, int C, int cap) {
+__global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, int C, int cap, int keys_held) {
     extern __shared__ uint32_t dyn[];  // lists of 16-bit rows (holes from the sink, survivors from the zone's end), images
     __shared__ EvictSmem sm;
     const int tid = threadIdx.x, part = blockIdx.x % C, head = blockIdx.x / C;
@@ -105,8 +105,24 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
     const int keep = zone - p.sink;                  // of them stay
     uint16_t *lists = reinterpret_cast<uint16_t *>(dyn);
     uint32_t *keys = dyn + cap;
-    const bool held = n * 4 <= kKeysBytes;
-    auto key = [&](int i) { return held ? keys[i] : key_of(mass[lo + i]); };
+    const bool held = n <= keys_held;  // the images, in shared memory
+    // f(candidate, image) for the candidates from, from + step, .. below to
+    auto each = [&](int from, int step, int to, auto &&f) {
+        if (held) {
+            for (int i = from; i < to; i += step) f(i, keys[i]);
+            return;
+        }
+        constexpr int U = 8;  // loads under way
+        for (int i = from; i < to; i += U * step) {
+            uint32_t k[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                k[u] = i + u * step < to ? key_of(mass[lo + i + u * step]) : 0u;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u * step < to) f(i + u * step, k[u]);
+        }
+    };
 
     // ---- the last candidate to stay: image T, place `last` among the candidates ----
     uint32_t T = 0xffffffffu;
@@ -152,10 +168,9 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
             want -= sm.above;
             __syncthreads();
             if (inside <= RANKED) {
-                for (int i = tid; i < n; i += THREADS) {
-                    const uint32_t k = key(i);
+                each(tid, THREADS, n, [&](int i, uint32_t k) {
                     if (k >= base && k - base <= span) sm.ranked[atomicAdd(&sm.count, 1u)] = make_uint2(k, i);
-                }
+                });
                 __syncthreads();
                 if (tid < (int)inside) {
                     const uint2 me = sm.ranked[tid];
@@ -177,12 +192,12 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
             if (shift == 0) {  // more equal images than can be ranked: the want-th of them in the order of the rows
                 const int per = ceil_div(n, THREADS), i0 = min(n, tid * per), i1 = min(n, i0 + per);
                 uint32_t eq = 0, all_eq;
-                for (int i = i0; i < i1; ++i) eq += key(i) == base;
+                each(i0, 1, i1, [&](int, uint32_t k) { eq += k == base; });
                 uint32_t seen = block_scan(eq, sm.warp_sum, &all_eq);
-                if (seen < want && want <= seen + eq) {
-                    for (int i = i0; i < i1; ++i)
-                        if (key(i) == base && ++seen == want) sm.row = i;
-                }
+                if (seen < want && want <= seen + eq)
+                    each(i0, 1, i1, [&](int i, uint32_t k) {
+                        if (k == base && ++seen == want) sm.row = i;
+                    });
                 __syncthreads();
                 T = base;
                 last = sm.row;
@@ -192,10 +207,9 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
             for (int i = 0; i < 4; ++i) sm.hist[i * THREADS + tid] = 0;
             __syncthreads();
             const int sub = shift == 21 ? 10 : 0;
-            for (int i = tid; i < n; i += THREADS) {
-                const uint32_t k = key(i);
+            each(tid, THREADS, n, [&](int, uint32_t k) {
                 if (k >= base && k - base <= span) atomicAdd(&sm.hist[(k - base) >> sub], 1u);
-            }
+            });
         }
     } else if (held) {
         for (int i = tid; i < n; i += THREADS) keys[i] = 0;
@@ -204,26 +218,23 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
 
     // ---- holes and the survivors that fill them: a contiguous run of candidates per thread, in row order ----
     const int per = ceil_div(n, THREADS), i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    auto stays = [&](int i) {
-        const uint32_t k = key(i);
-        return keep > 0 && (k > T || (k == T && i <= last));
-    };
+    auto stays = [&](int i, uint32_t k) { return keep > 0 && (k > T || (k == T && i <= last)); };
     uint32_t count = 0, total;  // holes in the upper half word, survivors in the lower
-    for (int i = i0; i < i1; ++i) {
-        const bool s = stays(i);
+    each(i0, 1, i1, [&](int i, uint32_t k) {
+        const bool s = stays(i, k);
         if (i < keep && !s) count += 1u << 16;
         if (i >= keep && s) count += 1;
-    }
+    });
     const uint32_t before = block_scan(count, sm.warp_sum, &total);
     const int moves = total & 0xffffu;
     uint16_t *holes = lists, *tails = lists + moves;
     uint32_t h = before >> 16, t = before & 0xffffu;
     if (count) {
-        for (int i = i0; i < i1; ++i) {
-            const bool s = stays(i);
+        each(i0, 1, i1, [&](int i, uint32_t k) {
+            const bool s = stays(i, k);
             if (i < keep && !s) holes[h++] = (uint16_t)i;
             if (i >= keep && s) tails[t++] = (uint16_t)(i - keep);
-        }
+        });
     }
     __syncthreads();
     if (C > 1) tc::cluster_sync();  // every CTA has read the masses
@@ -233,10 +244,20 @@ __global__ void __launch_bounds__(THREADS, 2) evict_kernel(const EvictParams p, 
     auto source = [&](int i) { return i < moves ? zone + tails[i] : N - p.recent + (i - moves); };
     auto target = [&](int i) { return i < moves ? p.sink + holes[i] : zone + (i - moves); };
     if (part == 0) {
-        for (int i = 0; i < rows; i += THREADS) {
-            const float m = i + tid < rows ? mass[source(i + tid)] : 0.f;
+        constexpr int U = 4;
+        for (int i0 = 0; i0 < rows; i0 += U * THREADS) {
+            float m[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * THREADS + tid;
+                m[u] = i < rows ? mass[source(i)] : 0.f;
+            }
             __syncthreads();
-            if (i + tid < rows) mass[target(i + tid)] = m;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * THREADS + tid;
+                if (i < rows) mass[target(i)] = m[u];
+            }
         }
     }
     // This CTA's columns of K and V: vectors [v0, v0 + vn) of a row of D/8, of K (x = 0) and V (x = 1) or of one of them.
@@ -294,8 +315,12 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     // Few heads: a cluster per head, so that the moves use more SMs (and more loads in flight).
     int C = 1;
     while (C < MAXC && heads * C * 2 <= 2 * kNumSMs) C *= 2;
-    const int smem = 4 * cap + min(4 * max(0, p.P_max - p.recent - p.sink), kKeysBytes);
-    cudaError_t e = allow_shared_memory<evict_kernel>(kMaxEvictRows / 2 * 4 + kKeysBytes);
+    // The images of a head's masses are held where they fit (16384 of them leave room for two CTAs on an SM; a longer
+    // cache's are read again from L2 by every pass: one head of 20000 rows: 85 us so, 38 held).
+    const int most = max(0, p.P_max - p.recent - p.sink), room = (kSmemBytes - 4 * cap) / 4;
+    const int keys_held = most <= room ? most : min(16384, room);
+    const int smem = 4 * cap + 4 * keys_held;
+    cudaError_t e = allow_shared_memory<evict_kernel>(kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(heads * C, 1, 1);
@@ -311,7 +336,7 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, evict_kernel, p, C, cap);
+    e = cudaLaunchKernelEx(&cfg, evict_kernel, p, C, cap, keys_held);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.B, 1, 1);
     cfg.blockDim = dim3(128, 1, 1);

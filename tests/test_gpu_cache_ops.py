@@ -522,6 +522,7 @@ EVICT = [  # L, B, Hkv, D, lens, budget, sink, recent
     (36, 1, 8, 128, [264], 256, 4, 16),
     (1, 1, 1, 128, [5000], 700, 0, 600),
     (1, 1, 2, 64, [9000], 8000, 16, 4000),
+    (1, 1, 1, 64, [30000], 20000, 3, 500),
     (1, 2, 1, 128, [700, 650], 600, 0, 600),
     (1, 2, 1, 128, [700, 650], 600, 600, 0),
     (3, 7, 3, 64, [64 * i + i for i in range(7)], 130, 3, 60),
