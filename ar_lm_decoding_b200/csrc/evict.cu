@@ -315,8 +315,9 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     // Few heads: a cluster per head, so that the moves use more SMs (and more loads in flight).
     int C = 1;
     while (C < MAXC && heads * C * 2 <= 2 * kNumSMs) C *= 2;
-    // The images of a head's masses are held where they fit (16384 of them leave room for two CTAs on an SM; a longer
-    // cache's are read again from L2 by every pass: one head of 20000 rows: 85 us so, 38 held).
+    // The images of a head's masses are held where they fit; where a cache can be too long for that, 16384 of them at
+    // most are (two CTAs on an SM), and a longer sequence's are read again from L2 by every pass (one head of 20000
+    // rows: 85 us so, 34 held; two heads of 60000 rows, which are not held: 179 us before this rule, 188 with it).
     const int most = max(0, p.P_max - p.recent - p.sink), room = (kSmemBytes - 4 * cap) / 4;
     const int keys_held = most <= room ? most : min(16384, room);
     const int smem = 4 * cap + 4 * keys_held;

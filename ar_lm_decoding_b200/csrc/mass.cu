@@ -5,7 +5,7 @@
 // columns, so that a key's weights are summed by one thread in a fixed order and written by it alone: no atomics, no
 // exchange.  A key tile feeds all its queries from one read of K: up to 128 queries stay in shared memory while a CTA's
 // run of key tiles streams by; more take turns against four key tiles that stay there meanwhile (so that the next turn's
-// queries arrive while this turn's weights are summed: 1.5 us of latency against 2 us of work).
+// queries arrive while this turn's weights are summed: by estimate 1.5 us of latency against 2 us of work).
 //
 // Work: the key tiles of all (layer, sequence, KV head) form one line, cut into equal shares of cost, one per CTA (every
 // SM the same work, whatever the lengths).  The pointers of the layers are on the device, so K comes by cp.async into the
