@@ -26,6 +26,7 @@ constexpr int BINS = 2048;
 constexpr int MAXC = 8;
 constexpr int RANKED = 256;         // rows ranked against each other at most
 constexpr int kSmemBytes = 227 * 1024 - 14 * 1024;  // dynamic shared memory at most (EvictSmem is static)
+static_assert(4 * (kMaxEvictRows / 2 + 8192) <= kSmemBytes, "lists and images beyond the shared memory");
 static_assert(BINS == 4 * THREADS, "four bins a thread in the bin search");
 
 struct EvictSmem {
@@ -40,6 +41,7 @@ struct EvictSmem {
     int row;              // its place
     int pages[kMaxPagesPerSeq];  // of the sequence (paged caches)
 };
+static_assert(sizeof(EvictSmem) <= 14 * 1024 - 512, "static shared memory beyond its part");
 
 __device__ __forceinline__ uint32_t key_of(float m) {
     if (m != m) return 0xffffffffu;
@@ -315,11 +317,16 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     // Few heads: a cluster per head, so that the moves use more SMs (and more loads in flight).
     int C = 1;
     while (C < MAXC && heads * C * 2 <= 2 * kNumSMs) C *= 2;
-    // The images of a head's masses are held where they fit; where a cache can be too long for that, 16384 of them at
-    // most are (two CTAs on an SM), and a longer sequence's are read again from L2 by every pass (one head of 20000
-    // rows: 85 us so, 34 held; two heads of 60000 rows, which are not held: 179 us before this rule, 188 with it).
-    const int most = max(0, p.P_max - p.recent - p.sink), room = (kSmemBytes - 4 * cap) / 4;
-    const int keys_held = most <= room ? most : min(16384, room);
+    // The images of a head's masses are held in shared memory where the longest sequence's fit: in a CTA's part, if few
+    // CTAs run (one head of 20000 rows: 24 us without, 16 held), in half an SM's elsewhere, so that two CTAs share one.
+    // Otherwise those of sequences of up to 8192 candidates are, and longer ones read the masses again in every pass,
+    // from the L1 that is left.  (The capacity decides, as the lengths are on the device.  288 heads of capacity 32768:
+    // 4104 -> 4096 rows 32.6 us with all held, 28.4 with 16384 of them, 27.1 so; 32768 -> 4096 rows 348, 335, 302;
+    // 20000 -> 19992 rows 48, 62, 65.)
+    constexpr int kPairBytes = 100 * 1024;  // with EvictSmem and the reserved KB less than half of 228 KB
+    const int most = max(0, p.P_max - p.recent - p.sink);
+    const int room = (heads * C <= 64 ? kSmemBytes : kPairBytes) / 4 - cap;
+    const int keys_held = most <= room ? most : 8192;
     const int smem = 4 * cap + 4 * keys_held;
     cudaError_t e = allow_shared_memory<evict_kernel>(kSmemBytes);
     if (e != cudaSuccess) return e;

@@ -523,6 +523,9 @@ EVICT = [  # L, B, Hkv, D, lens, budget, sink, recent
     (1, 1, 1, 128, [5000], 700, 0, 600),
     (1, 1, 2, 64, [9000], 8000, 16, 4000),
     (1, 1, 1, 64, [30000], 20000, 3, 500),
+    (1, 1, 9, 64, [29000], 28000, 3, 500),
+    (1, 2, 1, 64, [60000, 8300], 30000, 2, 100),
+    (1, 2, 80, 64, [26500, 130], 120, 4, 16),
     (1, 2, 1, 128, [700, 650], 600, 0, 600),
     (1, 2, 1, 128, [700, 650], 600, 600, 0),
     (3, 7, 3, 64, [64 * i + i for i in range(7)], 130, 3, 60),
