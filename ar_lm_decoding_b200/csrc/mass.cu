@@ -424,12 +424,15 @@ __global__ void __launch_bounds__(THREADS, 1) mass_kernel(const MassParams p) {
                     if (turn >= 2) ok = wait_free(q_empty(qb), ((turn >> 1) - 1) & 1);
                     if (ok && turn >= 4) ok = wait_free(l_empty(ls), ((turn >> 2) - 1) & 1);
                     if (!ok) break;
-                    {  // query c TQ + x is row j, head gq
+                    {  // query c TQ + x is row j, head gq; places past the last query repeat it (with -inf for its LSE: a
+                       // zero row would make a NaN of an infinity in K, and the last query sees every key that one does)
+                        const int e = c * TQ + nq - 1, je = e / p.G;
+                        const uint8_t *end = q + ((size_t)je * p.Hq + e - je * p.G) * (D * 2) + c16 * 16;
                         int j = (c * TQ + r0) / p.G, gq = c * TQ + r0 - j * p.G;
                         const uint8_t *at = q + ((size_t)j * p.Hq + gq) * (D * 2) + c16 * 16;
                         const uint32_t dst = sbase + qb * L::Q_BUF + dst0 - r0 * 128;
                         for (int x = r0; x < (nq + 31) / 32 * 32; x += RW) {
-                            copy16(dst + x * 128, x < nq ? at : q, x < nq);
+                            copy16(dst + x * 128, x < nq ? at : end);
                             at += RW * D * 2;
                             for (gq += RW; gq >= p.G; gq -= p.G) at += (size_t)(p.Hq - p.G) * (D * 2);
                         }

@@ -447,6 +447,25 @@ def test_attention_mass_sums_to_the_visible_share(abi):
     assert bool(((total - a * 4).abs() <= 2e-4 * a * 4).all())
 
 
+@pytest.mark.parametrize("D,R,Hq,Hkv", [(64, 3, 1, 1), (128, 5, 8, 2), (64, 77, 12, 2)])
+def test_attention_mass_of_keys_with_scores_of_minus_infinity(abi, D, R, Hq, Hkv):
+    """A cached key that holds an infinity and that every query scores -inf gets no weight, whatever the rows' number."""
+    n = 300
+    c = Caches(26, 1, 1, Hkv, D, [n])
+    q = _normal(c.g, 1, 1, R, Hq, D)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    keys = [0, 130, n - R - 1, n - 1]  # the last one is new: only the last query sees it
+    c.kc[0][0, :, keys, 0] = -float("inf")
+    lse = torch.full((1, 1, R, Hq), 6.0, device=DEV)
+    before = c.mass[0].clone()
+    c.add_mass(abi, q, lse, None, 0.5)
+    assert c.status.item() == 0
+    want = ref.mass_update(before[0], q[0, 0], lse[0, 0], c.kc[0][0], n, R, D**-0.5, 0.5)
+    got = c.mass[0][0].double()
+    assert bool((want[:, keys[:3]] == 0.5 * before[0][:, keys[:3]].double()).all()) and bool((want[:, n - 1] == 0).all())
+    assert bool(((got - want)[:, :n].abs() <= ref.MASS_RTOL * want[:, :n]).all())
+
+
 def test_attention_mass_wait_that_runs_out(abi):
     c = Caches(25, 2, 2, 2, 128, [700, 300])
     q, lse = _normal(c.g, 2, 2, 8, 4, 128), torch.full((2, 2, 8, 4), 6.0, device=DEV)
