@@ -585,9 +585,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp & 1) {
             // ================= MMA issue: warp 1 for row tile 0, warp 3 for row tile 1 =================
             // (The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.)
-            // The tensor core executes the MMAs that one thread issues in their order, so S of half tile u + 2 is issued
-            // right behind the PV of half tile u, whose P it overwrites.  S runs ahead of PV across segments too, so that
-            // the next segment's first scores are there when the softmax has written the last record.
+            // S of half tile u + 2 overwrites the P that the PV of half tile u reads, so it is issued once that PV has
+            // completed.  (Right behind it, on the order of issue alone: 61.3 against 63.0 us for 8 x Qwen3-8B k 8, the
+            // same elsewhere; that order is promised for MMAs of one shape and accumulator only.)  S runs ahead of PV
+            // across segments too, so that the next segment's first scores are there when the softmax has written the
+            // last record.
             const int t = __shfl_sync(0xffffffffu, warp >> 1, 0);
             constexpr uint32_t id_qk = tc::idesc_bf16_f32(TM, TH, 0, 0), id_pv = tc::idesc_bf16_f32(TM, D, 0, 1);
             const uint64_t dq = tc::smem_desc_sw128(sbase + t * L::Q_TILE, 16, 1024);
@@ -616,6 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             Cursor q{0, 0, 0, 0, 0, 0, -1, -1, false}, v{0, 0, 0, 0, 0, 0, -1, -1, false};
             int ns = 0;                  // segments of the PV
             uint32_t pph = 0, busy = 0;  // phases of p_full; S buffers (h of the half) whose PV is not issued yet
+            uint32_t read_ph = 0, reading = 0;  // phases of pv_done; S buffers whose PV is not known to have completed
             bool ok = true, more = true;
             auto read = [&](Cursor &c, Segment &sg) {  // segment c.seg
                 if (!wait(seg_full(c.seg % SEGS), (c.seg / SEGS) & 1)) return false;
@@ -674,6 +677,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ok = wait_full(q.ring);
                         if (!ok) break;
                     }
+                    if (reading >> q.h & 1) {
+                        ok = wait(pv_done(t, q.h), read_ph >> q.h & 1);
+                        if (!ok) break;
+                        read_ph ^= 1u << q.h;
+                        reading &= ~(1u << q.h);
+                        tc::fence_after_sync();
+                    }
                     if (one) issue_qk<D>(s_col + q.h * TH, dq, dk + st * kS + q.h * kHalf, id_qk);
                     commit(s_full(t, q.h));
                     busy |= 1u << q.h;
@@ -705,6 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::fence_after_sync();
                 if (one) issue_pv(o_col, s_col + h * TH, dv + st * kS + h * kHalf, id_pv, v.i > v.first || h > 0);
                 commit(pv_done(t, h));
+                reading |= 1u << h;
                 busy &= ~(1u << h);
                 if (++v.h == halves(v)) {
                     commit(empty(st));
