@@ -868,8 +868,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < D; j += 2)
                     a4[(j >> 1) & 3] = max3(a4[(j >> 1) & 3], fabsf(__uint_as_float(v[j >> 5][j & 31])),
                                             fabsf(__uint_as_float(v[j >> 5][(j + 1) & 31])));
-                const float amax = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
-                const float rs = amax > 0.f ? __fdividef(1.f, amax) : 0.f;
+                float amax = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
+                if (amax == INFINITY) {  // (V holds an infinity: the finite columns keep their values beside it)
+                    amax = 0.f;
+#pragma unroll
+                    for (int j = 0; j < D; ++j) {
+                        const float x = fabsf(__uint_as_float(v[j >> 5][j & 31]));
+                        if (x < INFINITY) amax = fmaxf(amax, x);
+                    }
+                }
+                const float rs = amax > 0.f ? __fdividef(1.f, amax) : 1.f;
                 if (valid) {
                     uint8_t *rec = p.ws + info + ((size_t)(cta + sg.id) * 2 + t) * tile_record_bytes(D);
                     uint4 *vals = reinterpret_cast<uint4 *>(rec) + row;
@@ -888,7 +896,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     reinterpret_cast<float2 *>(rec + TM * D * 2)[row] =
                         make_float2(l_run == 0.f ? -INFINITY : m_run + __log2f(l_run),  // (a NaN sum stays one)
-                                    l_run == 0.f ? 0.f : amax / l_run);
+                                    l_run == 0.f ? 0.f : amax > 0.f ? amax / l_run : 1.f / l_run);
                 }
             }
             tc::fence_before_sync();

@@ -175,10 +175,11 @@ size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, in
  *             (R = 1 is plain decoding, one token per sequence; R > 1 also
  *             scores or prefills R tokens)
  * q, k_new, v_new, out, lse  as in tidar_attn_step, with R rows per sequence.
- *             V rows multiply even a zero weight: a non-finite v_new, or a
- *             non-finite visible cache row, reaches every row of its sequence
- *             (a shared one, every row of the batch); masked k_new may hold
- *             anything.
+ *             V rows multiply even a zero weight: a non-finite element of v_new,
+ *             or of a visible cache row, reaches that element of every row of its
+ *             sequence (a shared one, of every row of the batch), as the infinity
+ *             it is where its weight is above zero, as NaN elsewhere, and no other
+ *             element; masked k_new may hold anything.
  * workspace   >= tidar_attn_shared_workspace_size(...) bytes, 256-byte aligned; what it
  *             held does not matter.  Calls that may run at the same time (two
  *             streams, two replayed graphs) need one each.

@@ -252,6 +252,32 @@ def test_shared_attention_masked_keys_may_hold_anything(abi):
     assert bool(torch.isnan(s.out[:, 6:9].float()).all())
 
 
+@pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
+def test_shared_attention_infinity_in_one_column_of_v(abi, paged):
+    """An infinity in V reaches its own column of the rows that see it, as an infinity, and no other column."""
+    for D, G in ((64, 2), (128, 3)):
+        s = Shared(abi, 57, 3, 2 * G, 2, D, 0, 5, 700, [300, 0, 40], paged=paged)
+        v, p = (s.vp, s.shared_table) if paged else (s.vs, None)
+        for col, x in ((3, math.inf), (D - 1, -math.inf)):  # shared row 70 of KV head 0
+            s.vs[0, 70, col] = x
+            if paged:
+                v[int(p[1]), 0, 6, col] = x
+        s.vc[0, 1, 17, 9] = math.inf  # own row 17 of sequence 0, KV head 1
+        if paged:
+            s.vp[int(s.table[0, 0]), 1, 17, 9] = math.inf
+        s.call()
+        assert s.status.item() == 0
+        want = torch.zeros_like(s.out, dtype=torch.float32)
+        want[:, :, :G, 3], want[:, :, :G, D - 1], want[0, :, G:, 9] = math.inf, -math.inf, math.inf
+        assert torch.equal(torch.where(want != 0, s.out.float(), 0.0), want)
+        for t in (s.vs, s.vc):
+            t[t.isinf()] = 0.0
+        out, lse, absum, vmax = s.reference()
+        off = (s.out.double() - out).abs() > ref.attn_tolerance(out, absum, vmax)
+        assert not bool((off & (want == 0)).any())
+        assert bool(((s.lse.double() - lse).abs() <= 1e-4).all())
+
+
 def test_shared_attention_bad_lengths_and_pages(abi):
     s = Shared(abi, 8, 3, 4, 2, 64, 2, 8, 100, [50, 60, 70])
     for bad in (-1, s.P_max + 1):
