@@ -278,6 +278,26 @@ def test_shared_attention_infinity_in_one_column_of_v(abi, paged):
         assert bool(((s.lse.double() - lse).abs() <= 1e-4).all())
 
 
+@pytest.mark.parametrize("v", [0.0, 2.0**-133, 2.0**-130, 2.0**-126, 2.0**-112, 9e37])
+def test_shared_attention_values_of_any_size(abi, v):
+    """Shared rows of V that are zero but for one element of size v, down to the smallest subnormal; then all of size v."""
+    s = Shared(abi, 50, 2, 4, 2, 64, 2, 8, 700, [300, 0])
+    s.vs[:, :s.S] = 0.0
+    s.vs[:, 3, 5] = v
+    if v < 1.0:
+        s.call()
+        assert s.status.item() == 0
+        s.check()
+    s = Shared(abi, 52, 1, 2, 1, 128, 0, 1, 2, [0])
+    s.q.zero_()  # (equal weights: the shared keys' partial row sums to 2 v)
+    s.vs[:], s.vn[:] = v, v
+    s.call()
+    out, lse, absum, vmax = s.reference()
+    err = (s.out.double() - out).abs()
+    # (sums below 2^-126 lose up to 2^-126 each: subnormal weights and products may count as zero)
+    assert bool((err <= ref.attn_tolerance(out, absum, vmax) + 2.0**-125).all())
+
+
 def test_shared_attention_bad_lengths_and_pages(abi):
     s = Shared(abi, 8, 3, 4, 2, 64, 2, 8, 100, [50, 60, 70])
     for bad in (-1, s.P_max + 1):
