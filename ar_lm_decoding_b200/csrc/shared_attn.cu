@@ -308,8 +308,14 @@ __device__ __forceinline__ float half_exp(const uint32_t (&u)[2][32], float sl2,
     return a + b;
 }
 
+// The weights are 2^(x - m) with m the row's running maximum plus kHeadroom: a maximum that is behind by up to 2^kHeadroom
+// leaves a half's weights below 1 in sum, and O below the number of halves times the largest |v|, as weights against the
+// true maximum would.  (With weights of up to 2^16, values of 1e33 overflowed.)
+constexpr float kHeadroom = 16.f;
+constexpr float kMaxHalfSum = 1.f;
+
 // The running max m of a row is raised to the maximum of the half at sc, where the row has none yet or its weights
-// against m sum to lt >= 2^16 (or are not finite), and O and the row's sum l are scaled to it.  (A call of its own: it is
+// against m sum to lt >= kMaxHalfSum (or are not finite), and O and the row's sum l are scaled to it.  (A call of its own: it is
 // rare, and inlined it would spread the loop over the instruction cache.)
 struct RowState {
     float m, l;
@@ -321,10 +327,10 @@ __device__ __noinline__ RowState raise_max(uint32_t sc, int k0, int lo, int glo,
     uint32_t u[2][32];
     load_scores(sc, u);
     mask_scores(u, k0, lo, glo, ghi);
-    const float mx = half_max(u) * sl2;
+    const float mx = half_max(u) * sl2 + kHeadroom;
     RowState st{m, l, 1};
     if (!(mx < INFINITY)) st.l = __int_as_float(0x7fffffff);  // a score of NaN or infinity: no softmax
-    const bool grow = mx > m && mx < INFINITY && (m == -INFINITY || !(lt < 65536.f));
+    const bool grow = mx > m && mx < INFINITY && (m == -INFINITY || !(lt < kMaxHalfSum));
     const float f = grow && m > -INFINITY ? fast_exp2(m - mx) : 1.f;
     if (__any_sync(0xffffffffu, f < 1.f)) {
         // O is at rest once the last half's PV has completed: the next one awaits this half's P
@@ -814,7 +820,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return ok;
             };
             // Exponentials of a half against the running max as it stands: a stale one is exact as long as the weights
-            // fit, whatever their size, so no maximum is taken while their sum stays below 2^16.
+            // fit, whatever their size, so no maximum is taken while their sum stays below kMaxHalfSum.
             auto softmax = [&](int h, bool masked, int lo, int glo, int ghi) {
                 const uint32_t sc = s_col + h * TH;
                 float lt = 0.f;
@@ -833,7 +839,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     load_scores(sc, u);
                     if (masked) mask_scores(u, h * TH, lo, glo, ghi);
                     lt = half_exp(u, sl2, m_run == -INFINITY ? 0.f : -m_run, pk);
-                    if (__all_sync(0xffffffffu, lt < 65536.f) || tries++ > 0) {
+                    if (__all_sync(0xffffffffu, lt < kMaxHalfSum) || tries++ > 0) {
                         tc::tmem_st32(sc, pk);
                         break;
                     }

@@ -180,6 +180,8 @@ size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, in
  *             sequence (a shared one, of every row of the batch), as the infinity
  *             it is where its weight is above zero, as NaN elsewhere, and no other
  *             element; masked k_new may hold anything.
+ *             Products are summed in fp32 before they are divided by the weights'
+ *             sum: the number of keys times the largest |v| must stay below 2^127.
  * workspace   >= tidar_attn_shared_workspace_size(...) bytes, 256-byte aligned; what it
  *             held does not matter.  Calls that may run at the same time (two
  *             streams, two replayed graphs) need one each.

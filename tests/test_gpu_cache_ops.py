@@ -298,6 +298,21 @@ def test_shared_attention_values_of_any_size(abi, v):
     assert bool((err <= ref.attn_tolerance(out, absum, vmax) + 2.0**-125).all())
 
 
+def test_shared_attention_weights_of_large_values(abi):
+    """V of 1e33 behind scores that grow by 2^9.5 after the first keys: the output stays within V's range."""
+    s = Shared(abi, 53, 4, 4, 4, 64, 0, 1, 0, [20000] * 4)
+    for x in (s.q, s.kn, s.kc):
+        x.zero_()
+    s.scale = 1.0
+    s.q[..., 0] = 8.0
+    s.kc[:, :, 64:20000, 0] = s.kn[..., 0] = 9.5 * math.log(2) / 8
+    s.vc[:, :, :20000] = 1e33 * torch.where(torch.arange(64, device=DEV) % 3 == 0, -1.0, 1.0)
+    s.vn.copy_(s.vc[:, :, 0][:, None])
+    s.call()
+    assert s.status.item() == 0
+    s.check()
+
+
 def test_shared_attention_bad_lengths_and_pages(abi):
     s = Shared(abi, 8, 3, 4, 2, 64, 2, 8, 100, [50, 60, 70])
     for bad in (-1, s.P_max + 1):
