@@ -465,6 +465,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::tma_prefetch_desc(&maps.q);
     }
     if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    // The rows of a Q tile past its G RT queries, which no copy fills, are zeros.  (What earlier launches left there could
+    // score NaN, so that the row never got a maximum and every half of its row tile was looked at twice: 4 sequences of k 8
+    // with 14 heads on 2 KV heads over 8000 shared keys took 54 to 67 us, 41 so.)
+    const int queries = g.RT * p.G, spare = (TM - queries) * (D / 8);
+    for (int i = tid; i < 2 * spare; i += THREADS) {
+        const int t = i >= spare, e = i - t * spare, row = queries + e / (D / 8), c = e % (D / 8);
+        *reinterpret_cast<uint4 *>(smem + t * L::Q_TILE + (c >> 3) * TM * 128 + row * 128 + ((c & 7) << 4)) =
+            make_uint4(0, 0, 0, 0);
+    }
+    if (spare > 0) tc::fence_proxy_async_smem();
     // every global read below waits for the previous kernel in the stream
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     int S = p.shared_len[0];
