@@ -299,6 +299,14 @@ tidar_status check_shared(int B, int Hq, int Hkv, int D, int R, int S_max, int P
     return TIDAR_OK;
 }
 
+// The sizes that only contiguous caches and only paged ones limit.
+bool contiguous_fits(int B, int Hkv, int S_max, int P_max) {
+    return (long long)Hkv * S_max < (1LL << 31) && (long long)B * Hkv * P_max < (1LL << 31);
+}
+bool pages_fit(int S_max, int P_max) {
+    return S_max <= kMaxSharedPages * kPageRows && P_max <= kMaxPagesPerSeq * kPageRows;
+}
+
 tidar_status attn_shared(SharedAttnParams p, int S_max, int P_max, size_t ws_bytes, float softmax_scale, void *stream,
                          long long wait_cycles = kCacheWaitCycles, int stall_test = 0) {
     if (!p.q || !p.k_new || !p.v_new || !p.shared_len || !p.prefix_len || !p.out || !p.dev_status)
@@ -333,6 +341,7 @@ tidar_status attn_shared(SharedAttnParams p, int S_max, int P_max, size_t ws_byt
 
 size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max) {
     if (check_shared(B, Hq, Hkv, D, R, S_max, P_max) != TIDAR_OK) return 0;
+    if (!contiguous_fits(B, Hkv, S_max, P_max) && !pages_fit(S_max, P_max)) return 0;
     return shared_attn_workspace_bytes(B, Hq, Hkv, D, R, S_max, P_max);
 }
 
@@ -343,8 +352,7 @@ static tidar_status attn_shared_contiguous(const void *q, const void *k_new, con
                                     void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream, long long wait_cycles, int stall_test) {
     const tidar_status st = check_shared(B, Hq, Hkv, D, R, S_max, P_max);
     if (st != TIDAR_OK) return st;
-    if ((long long)Hkv * S_max >= (1LL << 31) || (long long)B * Hkv * P_max >= (1LL << 31))
-        return TIDAR_ERR_UNSUPPORTED;
+    if (!contiguous_fits(B, Hkv, S_max, P_max)) return TIDAR_ERR_UNSUPPORTED;
     if (S_max > 0 && (!k_shared || !v_shared)) return TIDAR_ERR_INVALID_ARG;
     if (P_max > 0 && (!k_cache || !v_cache)) return TIDAR_ERR_INVALID_ARG;
     SharedAttnParams p{};

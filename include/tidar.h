@@ -146,7 +146,9 @@ tidar_status tidar_attn_step_paged(const void *q, const void *k_new, const void 
 
 /* Bytes of device scratch tidar_attn_step_shared (and its paged form, with
  * S_max = 64 * max_shared_pages and P_max = 64 * max_pages) needs for these
- * sizes; 0 for sizes those calls reject. */
+ * sizes; 0 for sizes that both calls reject.  (Sizes that only one of them
+ * takes, by its limit on contiguous rows or on pages, have room; the other call
+ * reports them.) */
 size_t tidar_attn_shared_workspace_size(int B, int Hq, int Hkv, int D, int R, int S_max, int P_max);
 
 /*
@@ -211,7 +213,8 @@ tidar_status tidar_attn_step_shared(const void *q, const void *k_new, const void
  * block_table   int32 [B, max_pages], pages of each sequence's own rows
  * A page id outside [0, num_pages) sets TIDAR_DEV_BAD_PAGE: among a sequence's
  * own pages that sequence's rows are not written, among the shared pages none
- * are.  Everything else as above.
+ * are.  num_pages * Hkv * 64 is below 2^31 here, in place of Hkv * S_max and
+ * B * Hkv * P_max (else TIDAR_ERR_UNSUPPORTED).  Everything else as above.
  */
 tidar_status tidar_attn_step_shared_paged(const void *q, const void *k_new, const void *v_new,
                                           const void *k_pool, const void *v_pool, const int32_t *shared_table,
@@ -509,8 +512,9 @@ tidar_status tidar_verify_commit(const void *p_logits, const void *q_logits, int
  *           or, with a block_table, pools [num_pages, Hkv, 64, D]
  * masses    device array of L device pointers, f32 [B, Hkv, P_max] each (P_max =
  *           64 * max_pages with a block_table), updated in place
- * block_table  int32 [B, max_pages] or NULL (contiguous caches; max_pages and
- *           num_pages are then ignored); P_max is ignored with a block_table
+ * block_table  int32 [B, max_pages], 1 <= max_pages <= 1024, or NULL (contiguous
+ *           caches; max_pages and num_pages are then ignored); P_max is ignored
+ *           with a block_table
  * prefix_len   int32 [B], after the commit
  * row_count    int32 [B], 0..min(R, prefix_len[b]) (accept_len of the verify), or
  *           NULL: R for every sequence
@@ -559,7 +563,7 @@ tidar_status tidar_attn_mass(const void *const *qs, const float *const *lses, co
  * budget, sink, recent >= 0 with sink + recent <= budget
  * dev_status  TIDAR_DEV_BAD_PREFIX, TIDAR_DEV_BAD_PAGE: that sequence is left
  *             untouched in every layer.
- * D in {64, 128}; P_max <= 65536 (else TIDAR_ERR_UNSUPPORTED); the caches
+ * D in {64, 128}; P_max <= 65536, L * B * Hkv <= 2^27 (else TIDAR_ERR_UNSUPPORTED); the caches
  * 16-byte aligned (the pointers are on the device: not checked).
  */
 tidar_status tidar_kv_evict(void *const *k_caches, void *const *v_caches, float *const *masses,

@@ -81,6 +81,34 @@ def test_shared_workspace(abi):
         assert abi.tidar_attn_shared_workspace_size(*bad) == 0
 
 
+def test_shared_workspace_sizes(abi):
+    """Every size that one of the two calls takes needs room; no size that both reject has any."""
+    size = abi.tidar_attn_shared_workspace_size
+    small = size(1, 1, 1, 64, 1, 0, 0)
+    assert small > 0
+    assert size(2, 4, 2, 64, 8, 256, 128) > small
+    assert size(1024, 8, 2, 128, 1, 4096 * 64, 65536) > size(1, 8, 2, 128, 1, 4096 * 64, 65536)
+    # too many rows for contiguous caches, not for pages: the contiguous call says so, the paged one takes the sizes
+    assert size(1024, 64, 32, 64, 1, 0, 65536) > 0
+    assert _shared(abi, B=1024, Hq=64, Hkv=32, mode=1, R=1, S_max=0, P_max=65536) == UNSUPPORTED
+    assert _shared_paged(abi, B=1024, Hq=64, Hkv=32, mode=1, R=1, msp=0, sht=None, mp=1024, ws_bytes=0) == WORKSPACE
+    for bad in ((1, 129, 1, 64, 1, 0, 0), (1, 1, 1, 64, 4097, 0, 0), (1025, 1, 1, 64, 1, 0, 0), (1, 1, 1, 64, 1, 0, -1),
+                (1, 0, 1, 64, 1, 0, 0), (1, 1, 0, 64, 1, 0, 0), (2, 4, 2, 64, 8, 1 << 30, 128),
+                (1024, 4, 2, 64, 8, 0, 1 << 20),
+                (1024, 1024, 8, 64, 4096, 0, 0)):
+        assert size(*bad) == 0, bad
+
+
+def test_limits_at_their_edges(abi):
+    """Sizes at a documented limit are taken, as the next check (a pointer that is missing) shows; one more is not."""
+    assert _evict(abi, L=1 << 17, B=1 << 5, Hkv=1 << 5, st=None) == INVALID
+    assert _evict(abi, L=(1 << 17) + 1, B=1 << 5, Hkv=1 << 5, st=None) == UNSUPPORTED
+    assert _evict(abi, P_max=65536, st=None) == INVALID and _evict(abi, bt=P, mp=1024, npg=4, st=None) == INVALID
+    assert _mass(abi, P_max=1 << 22, st=None) == INVALID and _mass(abi, bt=P, mp=1024, npg=4, st=None) == INVALID
+    assert _mass(abi, R=(1 << 29) - 1, st=None) == INVALID and _mass(abi, R=1 << 29, st=None) == UNSUPPORTED
+    assert _shared_paged(abi, npg=(1 << 24) - 1, kp=None) == INVALID and _shared_paged(abi, npg=1 << 24, kp=None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw", [dict(kp=None), dict(vp=None), dict(sht=None), dict(bt=None), dict(mp=0), dict(npg=0),
                                 dict(msp=-1), dict(R=7), dict(st=None)], ids=str)
 def test_shared_paged_invalid(abi, kw):
