@@ -731,6 +731,32 @@ def test_evict_offsets_past_32_bits(abi):
     assert torch.equal(vc[B - 1, :, 150:200], v0[:, n - 50:])
 
 
+@pytest.mark.parametrize("budget,sink,recent", [(200, 4, 50), (450, 0, 7)])
+def test_evict_keys_values_and_masses_past_32_bits(abi, budget, sink, recent):
+    """The last sequence's rows lie behind 4 Gi elements: its keys, its values and its masses all move, and nothing else."""
+    B, Hkv, D, P_max, n = 66, 8, 128, 65536, 500
+    g = _gen(36)
+    k, v = (torch.zeros((B, Hkv, P_max, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k[B - 1, :, :n], v[B - 1, :, :n] = _normal(g, Hkv, n, D), _normal(g, Hkv, n, D)
+    mass = torch.rand((B, Hkv, P_max), generator=g, device=DEV)
+    lens, st = _i32([0] * (B - 1) + [n]), _i32([0])
+    had = [t[B - 1, :, :n].clone() for t in (k, v, mass)]
+    others = mass[:B - 1].clone()
+    ptr = abi.pointer_array
+    abi.tidar_kv_evict(ptr([k], DEV), ptr([v], DEV), ptr([mass], DEV), None, 0, 0, lens, 1, B, Hkv, D, P_max, budget, sink,
+                       recent, st)
+    assert st.item() == 0 and lens.tolist() == [0] * (B - 1) + [budget]
+    for h in range(Hkv):
+        to, of = ref.evict_moves(had[2][h].tolist(), n, budget, sink, recent)
+        for got, was in zip((k, v, mass), had):
+            want = was[h].clone()
+            want[to] = was[h][of]
+            assert torch.equal(got[B - 1, h, :n], want)
+    for t in (k, v):
+        assert not bool(t[0].any()) and not bool(t[B - 2].any()) and not bool(t[B - 1, :, n:].any())
+    assert torch.equal(mass[:B - 1], others)
+
+
 @pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
 def test_decode_with_shared_prefix_and_bounded_caches(abi, paged):
     """The operators as a serving loop uses them: attention over [shared | own | new] in every layer, verify + commit,
