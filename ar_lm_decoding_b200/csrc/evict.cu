@@ -318,11 +318,13 @@ cudaError_t evict_launch(const EvictParams &p, cudaStream_t s) {
     int C = 1;
     while (C < MAXC && heads * C * 2 <= 2 * kNumSMs) C *= 2;
     // The images of a head's masses are held in shared memory where the longest sequence's fit: in a CTA's part, if few
-    // CTAs run (one head of 20000 rows: 24 us without, 16 held), in half an SM's elsewhere, so that two CTAs share one.
-    // Otherwise those of sequences of up to 8192 candidates are, and longer ones read the masses again in every pass,
-    // from the L1 that is left.  (The capacity decides, as the lengths are on the device.  288 heads of capacity 32768:
-    // 4104 -> 4096 rows 32.6 us with all held, 28.4 with 16384 of them, 27.1 so; 32768 -> 4096 rows 348, 335, 302;
-    // 20000 -> 19992 rows 48, 62, 65.)
+    // CTAs run, in half an SM's elsewhere, so that two CTAs share one.  Otherwise those of sequences of up to 8192
+    // candidates are, and longer ones read the masses again in every pass, from the L1 that is left.  The capacity decides,
+    // as the lengths are on the device.  Measured with the masses' copy beside it, held in a whole SM's part and not held:
+    // one head of capacity 20032, 20000 -> 12000 rows: 34 and 46 us; of 40064, 40000 -> 39992 rows: 34 and 95; 8 heads of
+    // it: 35 and 96; but also 9 heads of it, which are not held: 35 and 98, and 128 heads: 75 and 133.  Where caches are
+    // short against their capacity it is the other way round: 288 heads of capacity 32768, 4104 -> 4096 rows: 32.6 and 27.1;
+    // 32768 -> 4096 rows: 348 and 302; 20000 -> 19992 rows: 48 and 65.
     constexpr int kPairBytes = 100 * 1024;  // with EvictSmem and the reserved KB less than half of 228 KB
     const int most = max(0, p.P_max - p.recent - p.sink);
     const int room = (heads * C <= 64 ? kSmemBytes : kPairBytes) / 4 - cap;

@@ -14,8 +14,8 @@
 // A CTA (13 warps): warps 0-3 and 4-7 take the sums of every other key tile, warps 8-11 copy (K tiles through a ring of 4
 // to 8, Q through two buffers), warp 12 issues the MMAs into two TMEM buffers for each half of the summing warps.
 //
-// Bound by the bytes of K up to about 175 queries per key (a tile's 32 KB take an SM's share of HBM as long as 128 x 175
-// exponentials its MUFU), by the exponentials above.
+// Bound by the bytes of K up to about 175 queries per key at D = 128 (a tile's 32 KB take an SM's share of HBM as long as
+// 128 x 175 exponentials its MUFU) and 88 at D = 64, by the exponentials above.
 #include "cache_ops.cuh"
 #include "tc.cuh"
 
@@ -28,7 +28,7 @@ constexpr int TQ = 128;       // queries of a turn
 constexpr int THREADS = 416;
 constexpr int COPIERS = 128;  // threads of warps 8-11
 constexpr int GROUP = 4;      // key tiles that stay for several turns (at most the ring)
-constexpr int kBytesCost = 176;                  // cost of a tile that is bound by its bytes, in queries
+constexpr int kBytesCost = 176;  // cost of a tile that is bound by its bytes, in queries (at D = 64 too, where 88 would be it)
 constexpr int kSkip = 1 << 30;                   // in rows[b]: a page out of range
 
 template <int D>

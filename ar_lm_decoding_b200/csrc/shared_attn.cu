@@ -39,17 +39,17 @@ constexpr int THREADS = 384;
 constexpr int BOXR = kPageRows;
 // Cost of one key tile for a block of two row tiles and of one, and of a block's start and end (Q, the record), where
 // every CTA has a few tiles (see Line): measured ~3,300, ~2,900 and ~4,200 cycles, the ratio then tuned on the whole call
-// (8 x Qwen3-8B k 8: 66.3 us with 3 : 2 : 2, 60.5 with 8 : 7 : 10, 60.6 with 8 : 6 : 12; 16 single-token rows: 23.4, 23.0,
-// 22.3 us).
+// (8 x Qwen3-8B k 8: 69.5 us with 3 : 2 : 2, 62.3 with 8 : 7 : 10, 62.6 with 8 : 6 : 12; 16 single-token rows: 22.3, 21.5,
+// 21.5 us; 32 of them with 100 to 2000 rows of their own: 42.8, 41.6, 47.8; 16 x k 8, G 6, D 64: 41.3, 38.0, 37.1).
 constexpr int kLongBlock = 6;  // key tiles from which a block of a short line has two tiles a CTA
 constexpr int kCostPair = 8, kCostSingle = 6, kCostBlock = 12;
 
 // The line of key tiles (cum[b], beside it: key tiles of the sequences before b, nseq[b]: sequences before b that have
 // any).  Every CTA's share is at least the cost of one tile, so the CTAs from a block's first tile to its last all have
 // a part of it: where there are too few tiles for that every tile costs 1 and as many CTAs work as there are tiles, or
-// half as many where a block has many of them, so that its rows have fewer records to join (8 x Qwen2.5-1.5B k 4 over 8
-// shared and up to 9 own tiles: 21.7 us with a CTA per tile, 19.6 with one per two; 2 x the tiny shape, 1 and 2 tiles: 9.0
-// and 11.4).
+// half as many where a block has many of them, so that its rows have fewer records to join (8 x Qwen2.5-1.5B k 4: blocks of
+// 5 tiles take 15.0 us with a CTA per tile and 16.8 with one per two, of 6 tiles 16.7 and 14.2, of 9 tiles 20.4 and 18.6; two
+// single-token rows of Qwen3-8B, 5 tiles: 11.9 and 13.6, 6 tiles: 12.5 and 12.0, 8 tiles: 15.7 and 12.3).
 struct Line {
     int total;               // cost of all KV heads
     int head;                // cost of one KV head
