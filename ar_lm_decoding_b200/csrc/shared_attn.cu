@@ -380,15 +380,15 @@ __device__ __noinline__ void record_beside_infinities(uint32_t o_col, uint8_t *r
     for (int c = 0; c < D / 32; ++c) {
         tc::tmem_ld32(o_col + c * 32, v);
         tc::tmem_wait_ld();
-        if (!rec) continue;
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 h[e] = pack_half2(__uint_as_float(v[j + 2 * e]) * scale.x, __uint_as_float(v[j + 2 * e + 1]) * scale.x);
-            reinterpret_cast<uint4 *>(rec)[(c * 4 + j / 8) * TM + row] = make_uint4(h[0], h[1], h[2], h[3]);
+            if (rec) reinterpret_cast<uint4 *>(rec)[(c * 4 + j / 8) * TM + row] = make_uint4(h[0], h[1], h[2], h[3]);
         }
+        __syncwarp();  // (the next load is the whole warp's)
     }
     if (rec)
         reinterpret_cast<float2 *>(rec + TM * D * 2)[row] =
@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float amax = fmaxf(fmaxf(a4[0], a4[1]), fmaxf(a4[2], a4[3]));
                 const float2 scale = record_scale(amax);
                 uint8_t *rec = p.ws + info + ((size_t)(cta + sg.id) * 2 + t) * tile_record_bytes(D);
-                if (__any_sync(0xffffffffu, amax == INFINITY)) {
+                if (__any_sync(0xffffffffu, valid && amax == INFINITY)) {
                     record_beside_infinities<D>(o_col, valid ? rec : nullptr, row, m_run, l_run);
                 } else if (valid) {
                     uint4 *vals = reinterpret_cast<uint4 *>(rec) + row;
